@@ -73,6 +73,7 @@ typedef int32_t tq_status;
 #define TQ_ERR_NOT_CONVERGED 4   /* the codebook iteration did not converge */
 #define TQ_ERR_DEVICE_TIMEOUT 5  /* a bounded device-side wait gave up (see tq_sync_check) */
 #define TQ_ERR_WORKSPACE 6       /* workspace missing or smaller than the *_workspace_bytes value */
+#define TQ_ERR_DEVICE_INPUT 7    /* a kernel met an index outside its range in device data (see tq_sync_check) */
 
 /* element types of dense inputs / outputs */
 #define TQ_F32 0
@@ -306,6 +307,127 @@ TQ_API tq_status tq_attend_decode_noalloc(const tq_codebook* cb_k, const tq_code
                                    const uint32_t* v_signs, const uint16_t* v_norms, const uint16_t* v_gammas,
                                    float scale, float* out, void* stream);
 
+/* ---- rotary positions ---------------------------------------------------------------------------
+ * Not part of the TurboQuant write-ups: what a decoder applies to queries and keys before they meet
+ * the cache. Pair i of a head (i < rot_dim / 2) at position p is turned by the angle p f_i:
+ *   (a, b) -> (a cos - b sin, b cos + a sin);  coordinates from rot_dim on are left as they are. */
+#define TQ_ROPE_HALF 0    /* pair i = coordinates (i, i + rot_dim/2) */
+#define TQ_ROPE_PAIRS 1   /* pair i = coordinates (2i, 2i + 1) */
+#define TQ_ROPE_PLAIN 0   /* f_i = base^(-2i / rot_dim) */
+#define TQ_ROPE_LINEAR 1  /* f_i / factor: positions stretched over a longer context */
+#define TQ_ROPE_BLEND 2   /* by the turns original_len f_i / (2 pi) that a pair makes in the original context:
+                             f_i from high_turns up, f_i / factor up to low_turns, linear in the turns between */
+
+/* Table of the turns: table [n_pos][rot_dim/2][2] fp32, (cos, sin) of p f_i times `magnitude`, computed
+ * in fp64 and rounded once. rot_dim even, 2..512; factor > 0 (LINEAR, BLEND); 0 <= low_turns < high_turns
+ * and original_len > 0 (BLEND; ignored otherwise); n_pos may be 0. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+TQ_API tq_status tq_rope_table(int64_t n_pos, int32_t rot_dim, double base, int32_t scaling, double factor,
+                               double low_turns, double high_turns, double original_len, double magnitude,
+                               float* table, void* stream);
+
+/* Applies the table to x [tokens][heads][d] (dtype TQ_F32, TQ_BF16 or TQ_F16; element (t, h, i) at
+ * t * x_token_stride + h * x_head_stride + i), writing out (same dtype, strides of its own; out may be x with
+ * the same strides, any other overlap is not allowed). Token t is at positions[t]; a negative position
+ * marks a row that only pads the batch, whose output is left as it was. A position >= n_pos is reported by
+ * tq_sync_check (TQ_ERR_DEVICE_INPUT) and its row left as it was. inverse != 0 turns by the opposite
+ * angle: the gradient of x from the gradient of out. Products and sums in fp32, rounded once.
+ * d: 1..4096; 0 < rot_dim <= min(d, 512), even. Pointers aligned to their element (16-byte alignment of
+ * pointers and strides takes the vectorised form). tokens may be 0. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+TQ_API tq_status tq_rope(int64_t tokens, int32_t heads, int32_t d, int32_t rot_dim, int32_t layout,
+                         int32_t inverse, const void* x, int64_t x_token_stride, int64_t x_head_stride,
+                         int32_t dtype, const int32_t* positions, const float* table, int64_t n_pos, void* out,
+                         int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* ---- packed cache in pages ----------------------------------------------------------------------
+ * Pages of page_size token slots, shared by all sequences; slot s of the cache is offset
+ * s % page_size of page s / page_size. Every array holds the packed records of the layout above:
+ *   k_codes [num_pages][Hkv][page_size][d/32][b_k]   k_norms [num_pages][Hkv][page_size]
+ *   v_codes [num_pages][Hkv][page_size][d/32][b_v]   v_norms [num_pages][Hkv][page_size]
+ *   v_signs [num_pages][Hkv][page_size][d/32]        v_gammas [num_pages][Hkv][page_size]
+ * Keys by Algorithm 1 with cb_k (1..4 bits); values by Algorithm 1 with cb_v (1..4 bits; v_signs and
+ * v_gammas NULL) or by Algorithm 2 with cb_v its codebook (1..3 bits; both given).
+ * d 64 or 128; page_size a power of two in 16..1024.
+ *
+ * tq_paged_kv is the handle: host plain-old-data, filled by tq_paged_kv_init and then passed by
+ * pointer (it is copied into the launches). It holds the caller's pointers; the caller keeps the
+ * arrays alive and may fill the handle again at any time. */
+typedef struct tq_paged_kv {
+  int32_t d, Hkv, page_size, v_alg;      /* v_alg: 1 or 2, the values' algorithm */
+  int64_t num_pages;
+  uint32_t* k_codes;
+  uint16_t* k_norms;
+  uint32_t* v_codes;
+  uint32_t* v_signs;
+  uint16_t* v_norms;
+  uint16_t* v_gammas;
+  int32_t k_bits, v_bits;                /* bits of the two codebooks */
+  float ck[16], tk[16], cv[16], tv[16];  /* their fp32 levels and boundaries */
+  uint16_t k_half[16], v_half[16];       /* fp16 of unit * level: what the attention multiplies with */
+  float k_unit, v_unit;                  /* chosen so that these fp16 values are closest to proportional */
+  uint32_t ready;
+} tq_paged_kv;
+
+/* Checks the description of a cache and fills *kv. Host only. Errors: INVALID_ARG, UNSUPPORTED. */
+TQ_API tq_status tq_paged_kv_init(const tq_codebook* cb_k, const tq_codebook* cb_v, int32_t d, int32_t Hkv,
+                                  int32_t page_size, int64_t num_pages, uint32_t* k_codes, uint16_t* k_norms,
+                                  uint32_t* v_codes, uint32_t* v_signs, uint16_t* v_norms, uint16_t* v_gammas,
+                                  tq_paged_kv* kv);
+
+/* Appends the keys and values of `tokens` new tokens: token t's records go to slot slots[t] of every
+ * KV head, the key turned to positions[t] on the way (tq_rope's formula, without rounding the turned
+ * key). A record equals tq_encode_mse / tq_encode_prod of the (turned) vector, with every index and sign
+ * decided as in fp64. Norms are those of the (turned) vector.
+ *   k_new, v_new  [tokens][Hkv][d] in x_dtype (TQ_F32 or TQ_BF16); token t at t * k_token_stride
+ *                 (v_token_stride) elements, heads d apart; rows 16-byte aligned
+ *   slots         [tokens] int64; a negative slot marks a row that only pads the batch: nothing of it is
+ *                 written. A slot >= num_pages * page_size is reported by tq_sync_check
+ *                 (TQ_ERR_DEVICE_INPUT) and skipped. Two tokens of a call must not share a slot (the slot
+ *                 would hold a mixture of their records).
+ *   positions, table, n_pos, rot_dim, layout  as tq_rope, rot_dim <= d; rot_dim = 0 (positions and table
+ *                 NULL): keys are stored as they come. A position outside [0, n_pos) is reported and the
+ *                 token skipped.
+ *   rot           the prepared rotation for d
+ * tokens may be 0. Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t tokens, const void* k_new, int64_t k_token_stride,
+                                 const void* v_new, int64_t v_token_stride, int32_t x_dtype, const int64_t* slots,
+                                 const int32_t* positions, const float* table, int64_t n_pos, int32_t rot_dim,
+                                 int32_t layout, const void* rot, void* stream);
+
+/* Workspace bytes of tq_paged_attend for these sizes (0 for invalid sizes). */
+TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, int32_t Hq, int64_t total_q,
+                                              int32_t max_q_len, int64_t max_kv_len);
+
+/* Attention of new tokens over the paged cache: single tokens, chunks and mixtures of both in one call.
+ * Sequence b has kv_len[b] filled slots, its token t in page page_table[b][t / page_size] at offset
+ * t % page_size; its Qn = q_start[b+1] - q_start[b] newest tokens are the queries q_start[b] .. of q, query j
+ * at position pos = kv_len[b] - Qn + j:
+ *   x_t   = scale <q[j][h], k_hat_t>                        (k_hat, v_hat: the decoded records)
+ *   x_t   = softcap tanh(x_t / softcap)                     (softcap > 0)
+ *   x_t  += slopes[h] (t - pos)                             (slopes given: a bias by distance)
+ *   seen:   t < kv_len[b] and ((t <= pos and (window = 0 or t > pos - window)) or t < prefix_len[b])
+ *   out[j][h] = sum over seen t of softmax_t(x) v_hat_t;    0 where nothing is seen
+ *   q           [total_q][Hq][d] TQ_BF16, token i at i * q_token_stride elements, heads d apart
+ *   q_start     [B + 1] int32, increasing, from 0 on; rows of q from q_start[B] on are padding, their
+ *               outputs left as they were
+ *   kv_len      [B] int32;  page_table [B][max_pages] int32, read up to page (kv_len[b] - 1) / page_size
+ *   max_q_len, max_kv_len  at least the longest Qn and kv_len (they size the launch and the workspace)
+ *   prefix_len  [B] int32 or NULL: tokens before it are seen by every query
+ *   slopes      [Hq] fp32 or NULL
+ *   scale       0 (or any value that is not > 0) selects 1/sqrt(d)
+ *   out         [total_q][Hq][d] TQ_BF16, contiguous
+ * Lengths or page numbers outside their ranges are reported by tq_sync_check (TQ_ERR_DEVICE_INPUT); such
+ * tokens are taken as not seen. Scores, softmax and sums in fp32; queries, levels and softmax weights enter
+ * the tensor cores as fp16. Hq a multiple of Hkv, Hq / Hkv <= 128, B up to 65535. B and total_q may be 0.
+ * ws: caller device workspace of at least tq_paged_attend_workspace_bytes(...) bytes; calls that may
+ * overlap on the GPU (two streams, two captured graphs) need one each. Errors: INVALID_ARG, UNSUPPORTED,
+ * WORKSPACE, CUDA. */
+TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, int32_t Hq, int64_t total_q, int32_t max_q_len,
+                                 int64_t max_kv_len, const void* q, int64_t q_token_stride, int32_t q_dtype,
+                                 const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                                 int32_t max_pages, float scale, float softcap, int32_t window,
+                                 const int32_t* prefix_len, const float* slopes, const void* rot, void* out,
+                                 void* ws, size_t ws_bytes, void* stream);
+
 /* Self-test of the failure-detection path; no counterpart in the TurboQuant write-ups. Every
  * hand-off between the warps of a libtq kernel is a wait bounded in time: one that runs out records
  * an error and lets the kernel return, so a lost arrival is reported instead of hanging the GPU.
@@ -316,8 +438,9 @@ TQ_API tq_status tq_attend_decode_noalloc(const tq_codebook* cb_k, const tq_code
 TQ_API tq_status tq_selftest_wait(uint64_t limit_ns, void* stream);
 
 /* Synchronises `stream`, then reports a pending CUDA error (TQ_ERR_CUDA) or a device-side
- * timeout recorded by any libtq kernel since the last check (TQ_ERR_DEVICE_TIMEOUT, which this
- * call clears). TQ_OK otherwise. */
+ * timeout recorded by any libtq kernel since the last check (TQ_ERR_DEVICE_TIMEOUT) or an index
+ * outside its range that a kernel met in device data (TQ_ERR_DEVICE_INPUT); it clears what it
+ * reports. TQ_OK otherwise. */
 TQ_API tq_status tq_sync_check(void* stream);
 
 #ifdef __cplusplus

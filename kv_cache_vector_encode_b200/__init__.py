@@ -22,8 +22,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtq.so")
 
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA = 0, 1, 2, 3
-TQ_ERR_NOT_CONVERGED, TQ_ERR_DEVICE_TIMEOUT, TQ_ERR_WORKSPACE = 4, 5, 6
+TQ_ERR_NOT_CONVERGED, TQ_ERR_DEVICE_TIMEOUT, TQ_ERR_WORKSPACE, TQ_ERR_DEVICE_INPUT = 4, 5, 6, 7
 TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
+TQ_ROPE_HALF, TQ_ROPE_PAIRS = 0, 1
+TQ_ROPE_PLAIN, TQ_ROPE_LINEAR, TQ_ROPE_BLEND = 0, 1, 2
 
 
 class TQError(RuntimeError):
@@ -51,11 +53,27 @@ class Codebook(ctypes.Structure):
         return list(self.t)[: self.levels - 1]
 
 
+class _PagedKV(ctypes.Structure):
+    """Mirror of tq_paged_kv (host POD)."""
+    _fields_ = [
+        ("d", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("page_size", ctypes.c_int32), ("v_alg", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("k_codes", ctypes.c_void_p), ("k_norms", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("v_signs", ctypes.c_void_p), ("v_norms", ctypes.c_void_p), ("v_gammas", ctypes.c_void_p),
+        ("k_bits", ctypes.c_int32), ("v_bits", ctypes.c_int32),
+        ("ck", ctypes.c_float * 16), ("tk", ctypes.c_float * 16), ("cv", ctypes.c_float * 16), ("tv", ctypes.c_float * 16),
+        ("k_half", ctypes.c_uint16 * 16), ("v_half", ctypes.c_uint16 * 16),
+        ("k_unit", ctypes.c_float), ("v_unit", ctypes.c_float), ("ready", ctypes.c_uint32),
+    ]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
 _I32, _I64, _SZ, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _CB = ctypes.POINTER(Codebook)
+_KV = ctypes.POINTER(_PagedKV)
+_D = ctypes.c_double
 
 _SIGNATURES = {
     "tq_last_error": (ctypes.c_char_p, []),
@@ -82,6 +100,13 @@ _SIGNATURES = {
     "tq_attend_append_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I64, _I32, _I32, _I32]),
     "tq_attend_append": (_I32, [_CB, _CB, _I32, _I32, _I32, _I64, _I64, _I32, _P, _I32, _P, _P, _I32, _P, _P, _P,
                                 _P, _P, _P, _P, _F, _P, _P, _SZ, _P]),
+    "tq_rope_table": (_I32, [_I64, _I32, _D, _I32, _D, _D, _D, _D, _D, _P, _P]),
+    "tq_rope": (_I32, [_I64, _I32, _I32, _I32, _I32, _I32, _P, _I64, _I64, _I32, _P, _P, _I64, _P, _I64, _I64, _P]),
+    "tq_paged_kv_init": (_I32, [_CB, _CB, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _P, _P, _KV]),
+    "tq_paged_append": (_I32, [_KV, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _P, _I64, _I32, _I32, _P, _P]),
+    "tq_paged_attend_workspace_bytes": (_SZ, [_KV, _I32, _I32, _I64, _I32, _I64]),
+    "tq_paged_attend": (_I32, [_KV, _I32, _I32, _I64, _I32, _I64, _P, _I64, _I32, _P, _P, _P, _I32, _F, _F, _I32, _P,
+                               _P, _P, _P, _P, _SZ, _P]),
     "tq_selftest_wait": (_I32, [ctypes.c_uint64, _P]),
     "tq_sync_check": (_I32, [_P]),
 }
@@ -368,6 +393,168 @@ def tq_attend_append(cb_k: Codebook, cb_v: Codebook, q, rot, k_new, v_new, T_cur
                                   _ptr(out, "out", [torch.float32]), _ptr(ws, "ws"), ws.numel(), _stream(stream)))
 
 
+# ---- rotary positions, packed cache in pages -----------------------------------------------------
+
+def _on(device, dtype, **tensors):
+    """Checks of the calls below: each tensor given is on `device`, contiguous and of `dtype`; the device is
+    the current one (the calls launch there)."""
+    for name, t in tensors.items():
+        if t is not None and (t.dtype is not dtype or t.device != device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+
+
+def _current(t, name):
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t.device
+
+
+def tq_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: int = TQ_ROPE_PLAIN, factor: float = 1.0,
+                  low_turns: float = 1.0, high_turns: float = 32.0, original_len: float = 0.0,
+                  magnitude: float = 1.0, device="cuda", stream=None):
+    """Table [n_pos, rot_dim // 2, 2] float32 of (cos, sin) for tq_rope and tq_paged_append."""
+    import torch
+    device = torch.device(device)
+    table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    _current(table, "device")
+    _check(lib().tq_rope_table(n_pos, rot_dim, base, scaling, factor, low_turns, high_turns, original_len, magnitude,
+                               table.data_ptr(), _stream(stream)))
+    return table
+
+
+def tq_rope(x, positions, table, out=None, layout: int = TQ_ROPE_HALF, inverse: bool = False, stream=None):
+    """Turns the heads of x [tokens, heads, d] (float32 / bfloat16 / float16, last axis contiguous) to positions
+    [tokens] (int32; negative: a padding row, left as it is). out: x itself by default (in place).
+    inverse=True turns the other way: the gradient with respect to x."""
+    import torch
+    device = _current(x, "x")
+    if out is None:
+        out = x
+    if x.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError(f"x: dtype {x.dtype} not float32 / bfloat16 / float16")
+    tokens, heads, d = x.shape
+    if out.shape != x.shape or out.dtype is not x.dtype or out.device != device:
+        raise ValueError("out must have the shape, dtype and device of x")
+    if x.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("the last axis of x and out must be contiguous")
+    _on(device, torch.int32, positions=positions)
+    _on(device, torch.float32, table=table)
+    if positions.shape != (tokens,) or table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("positions must be [tokens] and table [n_pos, rot_dim // 2, 2]")
+    _check(lib().tq_rope(tokens, heads, d, 2 * table.shape[1], layout, 1 if inverse else 0, x.data_ptr(), x.stride(0),
+                         x.stride(1), _xdtype(x), positions.data_ptr(), table.data_ptr(), table.shape[0],
+                         out.data_ptr(), out.stride(0), out.stride(1), _stream(stream)))
+    return out
+
+
+class PagedKV:
+    """Handle of a packed cache in pages (tq_paged_kv): k_codes [pages, Hkv, page_size, d/32, b_k] int32,
+    k_norms [pages, Hkv, page_size] float16, v_codes, v_norms likewise; v_signs [pages, Hkv, page_size, d/32]
+    and v_gammas for values by Algorithm 2. It keeps the tensors alive."""
+
+    def __init__(self, cb_k: Codebook, cb_v: Codebook, k_codes, k_norms, v_codes, v_norms, v_signs=None, v_gammas=None):
+        import torch
+        self.device = _current(k_codes, "k_codes")
+        if k_codes.dim() != 5:
+            raise ValueError("k_codes must be [pages, Hkv, page_size, d/32, bits]")
+        at, groups = tuple(k_codes.shape[:3]), k_codes.shape[3]
+        if (v_signs is None) != (v_gammas is None):
+            raise ValueError("v_signs and v_gammas go together")
+        for name, t, shape in (("k_codes", k_codes, (*at, groups, cb_k.bits)), ("v_codes", v_codes, (*at, groups, cb_v.bits)),
+                               ("k_norms", k_norms, at), ("v_norms", v_norms, at), ("v_signs", v_signs, (*at, groups)),
+                               ("v_gammas", v_gammas, at)):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        _on(self.device, torch.int32, k_codes=k_codes, v_codes=v_codes, v_signs=v_signs)
+        _on(self.device, torch.float16, k_norms=k_norms, v_norms=v_norms, v_gammas=v_gammas)
+        self.tensors = (k_codes, k_norms, v_codes, v_norms, v_signs, v_gammas)
+        self.num_pages, self.Hkv, self.page_size = at
+        self.d = 32 * groups
+        self.struct = _PagedKV()
+        ptr = [None if t is None else t.data_ptr() for t in (k_codes, k_norms, v_codes, v_signs, v_norms, v_gammas)]
+        _check(lib().tq_paged_kv_init(ctypes.byref(cb_k), ctypes.byref(cb_v), self.d, self.Hkv, self.page_size,
+                                      self.num_pages, *ptr, ctypes.byref(self.struct)))
+        self.ref = ctypes.byref(self.struct)
+
+
+def tq_paged_append(kv: PagedKV, k_new, v_new, slots, rot, positions=None, table=None, layout: int = TQ_ROPE_HALF,
+                    stream=None):
+    """Encodes k_new, v_new [tokens, Hkv, d] (float32 / bfloat16) into slots [tokens] (int64; negative: a padding
+    row) of the cache, the keys turned to `positions` (int32) with `table` on the way where they are given."""
+    import torch
+    if kv.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {kv.device}, which is not the current device")
+    tokens = k_new.shape[0]
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.shape != (tokens, kv.Hkv, kv.d) or t.dtype is not k_new.dtype or t.device != kv.device:
+            raise ValueError(f"{name} must be [tokens, {kv.Hkv}, {kv.d}] on {kv.device}, both of one dtype")
+        if t.stride(2) != 1 or (kv.Hkv > 1 and t.stride(1) != kv.d):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if k_new.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"k_new: dtype {k_new.dtype} not float32 / bfloat16")
+    if (positions is None) != (table is None):
+        raise ValueError("positions and table go together")
+    _on(kv.device, torch.int64, slots=slots)
+    _on(kv.device, torch.int32, positions=positions)
+    _on(kv.device, torch.float32, table=table)
+    if slots.shape != (tokens,) or (positions is not None and positions.shape != (tokens,)):
+        raise ValueError("slots and positions must be [tokens]")
+    if table is not None and (table.dim() != 3 or table.shape[2] != 2):
+        raise ValueError("table must be [n_pos, rot_dim // 2, 2]")
+    row = kv.Hkv * kv.d                                  # a single token may have any stride
+    ks, vs = (t.stride(0) if tokens > 1 else row for t in (k_new, v_new))
+    _check(lib().tq_paged_append(kv.ref, tokens, k_new.data_ptr(), ks, v_new.data_ptr(), vs, _xdtype(k_new),
+                                 slots.data_ptr(), None if positions is None else positions.data_ptr(),
+                                 None if table is None else table.data_ptr(), 0 if table is None else table.shape[0],
+                                 0 if table is None else 2 * table.shape[1], layout, _ptr(rot, "rot"), _stream(stream)))
+
+
+def tq_paged_attend_workspace_bytes(kv: PagedKV, B: int, Hq: int, total_q: int, max_q_len: int, max_kv_len: int) -> int:
+    return int(lib().tq_paged_attend_workspace_bytes(kv.ref, B, Hq, total_q, max_q_len, max_kv_len))
+
+
+def tq_paged_attend(kv: PagedKV, q, q_start, kv_len, page_table, rot, out, max_q_len: int, max_kv_len: int, scale=None,
+                    softcap: float = 0.0, window: int = 0, prefix_len=None, slopes=None, ws=None, stream=None):
+    """Attention of the newest tokens of B sequences over the paged cache: q [total_q, Hq, d] bfloat16 (token stride
+    free), out the same, contiguous; q_start [B + 1], kv_len [B], page_table [B, max_pages], prefix_len [B] int32;
+    slopes [Hq] float32."""
+    import torch
+    if kv.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {kv.device}, which is not the current device")
+    total_q, Hq, d = q.shape
+    if d != kv.d or q.dtype is not torch.bfloat16 or q.device != kv.device:
+        raise ValueError(f"q must be bfloat16 [total_q, Hq, {kv.d}] on {kv.device}")
+    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != d):
+        raise ValueError("q: the heads of a token must be contiguous")
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    _on(kv.device, torch.bfloat16, out=out)
+    _on(kv.device, torch.int32, q_start=q_start, kv_len=kv_len, page_table=page_table, prefix_len=prefix_len)
+    _on(kv.device, torch.float32, slopes=slopes)
+    B = kv_len.shape[0]
+    if q_start.shape != (B + 1,) or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("q_start must be [B + 1], kv_len [B] and page_table [B, max_pages]")
+    if prefix_len is not None and prefix_len.shape != (B,):
+        raise ValueError("prefix_len must be [B]")
+    if slopes is not None and slopes.shape != (Hq,):
+        raise ValueError("slopes must be [Hq]")
+    if ws is None:
+        ws = torch.empty(max(tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len), 16),
+                         dtype=torch.uint8, device=q.device)
+    elif ws.device != kv.device:
+        raise ValueError(f"ws must be on {kv.device}")
+    _check(lib().tq_paged_attend(kv.ref, B, Hq, total_q, max_q_len, max_kv_len, q.data_ptr(),
+                                 q.stride(0) if total_q > 1 else Hq * d, TQ_BF16, q_start.data_ptr(), kv_len.data_ptr(),
+                                 page_table.data_ptr(), page_table.shape[1], 0.0 if scale is None else float(scale),
+                                 float(softcap), window, None if prefix_len is None else prefix_len.data_ptr(),
+                                 None if slopes is None else slopes.data_ptr(), _ptr(rot, "rot"), out.data_ptr(),
+                                 _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream)))
+    return out
+
+
 def tq_sync_check(stream=None):
     _check(lib().tq_sync_check(_stream(stream)))
 
@@ -394,3 +581,21 @@ def empty_prod(n: int, d: int, bits: int, device="cuda"):
             torch.empty((n, d // 32), dtype=torch.int32, device=device),
             torch.empty((n,), dtype=torch.float16, device=device),
             torch.empty((n,), dtype=torch.float16, device=device))
+
+
+def empty_paged(num_pages: int, Hkv: int, page_size: int, d: int, k_bits: int, v_bits: int, v_alg: int = 2, device="cuda"):
+    """A PagedKV with new arrays: keys by Algorithm 1 at k_bits, values by Algorithm v_alg at v_bits (Algorithm 2
+    with the codebook of v_bits - 1 bits)."""
+    import torch
+    vb = v_bits - 1 if v_alg == 2 else v_bits
+    at = (num_pages, Hkv, page_size)
+
+    def words(*shape):
+        return torch.empty((*at, *shape), dtype=torch.int32, device=device)
+
+    def halves():
+        return torch.empty(at, dtype=torch.float16, device=device)
+
+    signs = (words(d // 32), halves()) if v_alg == 2 else (None, None)
+    return PagedKV(tq_codebook_init(d, k_bits), tq_codebook_init(d, vb), words(d // 32, k_bits), halves(),
+                   words(d // 32, vb), halves(), *signs)

@@ -1,0 +1,94 @@
+// Shared by the kernels of tq_paged_attend: the call's parameters and what a query row may see.
+#pragma once
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "sm100.cuh"
+
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct PagedAttendParams {
+  const uint32_t* k_codes;
+  const uint16_t* k_norms;
+  const uint32_t* v_codes;
+  const uint32_t* v_signs;
+  const uint16_t* v_norms;
+  const uint16_t* v_gammas;
+  int64_t num_pages, total_q, max_kv, q_stride;
+  int page_shift, Hkv, Hq, g, B, max_pages, max_q, window;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* table;
+  const int32_t* prefix;
+  const float* slopes;
+  const uint16_t* q;           // bf16
+  uint16_t* out;               // bf16
+  float scale_log2;            // scale log2(e) / k_unit
+  float cap2x, cap_log2;       // 2 / cap, cap log2(e) (cap = 0: none)
+  float v_inv_unit, alpha;
+  uint32_t ktab[4], vtab[4];   // level tables for byte permutes: low bytes of levels 0-3, 4-7, high bytes
+  const float* Pi;
+  const float* S;
+  const uint8_t* img[6];       // Pi_hi, Pi_lo, PiT_hi, PiT_lo, ST_hi, ST_lo shared-memory images
+  __half* qr;                  // rotated queries [total_q * Hq][d], scaled by a power of two per row
+  float* qs;                   // that scale's inverse [total_q * Hq]
+  float2* ml;                  // partial (reference, sum) [total_q * Hq][nsplit]
+  float* po;                   // partial outputs [total_q * Hq][nsplit][parts d]
+  int nsplit, span;            // splits of the visible tokens, tokens of each
+  uint32_t* err;
+};
+
+// One sequence of the call, its lengths checked against the limits the launch was sized for.
+struct PagedSeq {
+  int q0, qn;                  // first query row, number of queries
+  int64_t kv;                  // filled slots
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b) {
+  PagedSeq s;
+  s.q0 = p.q_start[b];
+  int q1 = p.q_start[b + 1];
+  int64_t kv = p.kv_len[b];
+  const int64_t most = min(p.max_kv, (int64_t)p.max_pages << p.page_shift);
+  bool bad = false;
+  if (s.q0 < 0 || q1 < s.q0 || q1 > p.total_q || q1 - s.q0 > p.max_q) {
+    bad = true;
+    s.q0 = q1 = 0;
+  }
+  if (kv < 0 || kv > most) {
+    bad = true;
+    kv = kv < 0 ? 0 : most;
+  }
+  if (bad && threadIdx.x == 0) atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+  s.qn = q1 - s.q0;
+  s.kv = kv;
+  return s;
+}
+
+// Tokens [lo, hi) that the queries at positions [p0, p1] of a sequence may see between them.
+__device__ __forceinline__ void paged_range(const PagedAttendParams& p, const PagedSeq& s, int64_t p0, int64_t p1,
+                                            int64_t prefix, int64_t& lo, int64_t& hi) {
+  hi = min(s.kv, max(p1 + 1, prefix));
+  lo = p.window > 0 && prefix <= 0 ? max((int64_t)0, p0 - p.window + 1) : 0;
+  if (hi < lo) hi = lo;
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap tanh(x / cap) in log2 units, from x2 = 2 log2(e) x / cap: tanh(u) = 1 - 2 / (e^(2u) + 1). Its error is
+// absolute, about 2^-23 of the cap, which is what a softmax needs of its scores.
+__device__ __forceinline__ float capped(float x2, float cap_log2) {
+  return cap_log2 - __fdividef(2.0f * cap_log2, ex2_approx(fminf(x2, 100.0f)) + 1.0f);
+}
+#endif
+
+}  // namespace tq

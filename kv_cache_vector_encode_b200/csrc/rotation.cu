@@ -168,6 +168,8 @@ extern "C" TQ_API tq_status tq_sync_check(void* stream) {
   if ((e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v))) != cudaSuccess) return cuda_fail(e, "tq_sync_check");
   if (v != 0) {
     cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
+    if (v == kDevBadInput)
+      return fail(TQ_ERR_DEVICE_INPUT, "a libtq kernel met a position, slot, page or length out of range");
     return fail(TQ_ERR_DEVICE_TIMEOUT, "a libtq kernel gave up a bounded wait (device code " + std::to_string(v) + ")");
   }
   return TQ_OK;

@@ -76,4 +76,8 @@ tq_status attend_impl(const char* f, const tq_codebook* cb_k, const tq_codebook*
                       const uint16_t* v_norms, const uint16_t* v_gammas, float scale, float* out, void* ws,
                       size_t ws_bytes, void* stream);
 
+// Paged cache (paged.cpp): whether a handle has been filled by tq_paged_kv_init.
+constexpr uint32_t kPagedReady = 0x54515047u;   // "TQPG"
+inline bool paged_ready(const tq_paged_kv* kv) { return kv && kv->ready == kPagedReady; }
+
 }  // namespace tq
