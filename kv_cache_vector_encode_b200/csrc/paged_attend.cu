@@ -75,40 +75,6 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Level indices as nibbles: nibble n of the result = index of coordinate s + 4 n (n = 0..3 from a shift of 16 h
-// + s). For 16 levels the nibble is the magnitude's index and `neg` has bit 0 of nibble n set where the
-// level is negative.
-template <int BITS>
-__device__ __forceinline__ uint32_t pick(const uint32_t* w, int shift, uint32_t& neg) {
-  uint32_t x = 0;
-  if constexpr (BITS == 4) {
-    neg = (~w[3] >> shift) & 0x11111111u;
-    const uint32_t f = ~w[3];
-#pragma unroll
-    for (int b = 0; b < 3; ++b) x |= (((w[b] ^ f) >> shift) & 0x11111111u) << b;
-  } else {
-#pragma unroll
-    for (int b = 0; b < BITS; ++b) x |= ((w[b] >> shift) & 0x11111111u) << b;
-    neg = 0;
-  }
-  return x;
-}
-// Four levels from the low four nibbles of `sel`: (0, 1) and (2, 3) as fp16 pairs.
-template <int BITS>
-__device__ __forceinline__ void look_up(uint32_t sel, uint32_t neg, const uint32_t (&tab)[4], uint32_t& p0, uint32_t& p1) {
-  uint32_t lb, hb;
-  if constexpr (BITS <= 2) {
-    lb = __byte_perm(tab[0], 0u, sel);
-    hb = __byte_perm(tab[2], 0u, sel);
-  } else {
-    lb = __byte_perm(tab[0], tab[1], sel);
-    hb = __byte_perm(tab[2], tab[3], sel);
-  }
-  if constexpr (BITS == 4) hb ^= __byte_perm(0x8000u, 0u, neg);
-  p0 = __byte_perm(lb, hb, 0x5140u);
-  p1 = __byte_perm(lb, hb, 0x7362u);
-}
-
 template <int D, int KB, int VB, bool ALG2>
 struct Stage {   // 32-bit words of a 16-token stage
   static constexpr int G = D / 32;
@@ -130,7 +96,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const __grid_const
   const int b = blockIdx.z / p.Hkv, hkv = blockIdx.z % p.Hkv;
   const PagedSeq sq = paged_seq(p, b);
   const int rows = sq.qn * p.g, row0 = blockIdx.y * kRows;
-  if (row0 >= rows) return;
+  if (row0 >= rows || rows > p.chunk_rows) return;
   const int64_t first = sq.kv - sq.qn;                           // position of query 0
   const int64_t prefix = p.prefix ? min((int64_t)p.prefix[b], sq.kv) : 0;
   const int jlo = row0 / p.g, jhi = min(rows - 1, row0 + kRows - 1) / p.g;
@@ -140,6 +106,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const __grid_const
   const int64_t t1 = min(hi, t0 + p.span);
   const int nblk = t1 > t0 ? (int)((t1 - t0 + 15) >> 4) : 0;
 
+  const int64_t slot0 = (int64_t)blockIdx.z * p.row_slots;       // this unit's rows in the workspace
   // this lane's two query rows (2c, 2c + 1 of the block)
   int64_t pos[2];
   float fac[2], slope[2], ref[2], sum[2], wsum[2] = {0.f, 0.f}, zsum[2] = {0.f, 0.f};
@@ -149,7 +116,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const __grid_const
     const bool on = row < rows;
     const int j = on ? row / p.g : 0, h = hkv * p.g + (on ? row - j * p.g : 0);
     pos[u] = on ? first + j : -1;
-    fac[u] = on ? p.scale_log2 * p.qs[(int64_t)(sq.q0 + j) * p.Hq + h] : 0.f;
+    fac[u] = on ? p.scale_log2 * p.qs[slot0 + row] : 0.f;
     slope[u] = on && p.slopes ? p.slopes[h] * kLog2e : 0.f;
     ref[u] = -INFINITY;
     sum[u] = 0.f;
@@ -161,8 +128,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const __grid_const
   {
     const int row = row0 + r;
     const bool on = row < rows;
-    const int j = on ? row / p.g : 0, h = hkv * p.g + (on ? row - j * p.g : 0);
-    const __half* q = p.qr + ((int64_t)(sq.q0 + j) * p.Hq + h) * D + c * (D / 4);
+    const __half* q = p.qr + (slot0 + (on ? row : 0)) * D + c * (D / 4);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const int at = D == 128 ? (ks >> 1) + 16 * (ks & 1) : ks;
@@ -464,28 +430,30 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rows_kernel(const __grid_const
       o += f * m[i];
       l += f * m[PD + 1];
     }
-    const int j = (row0 + row) / p.g, h = hkv * p.g + (row0 + row) - j * p.g;
-    const int64_t at = ((int64_t)(sq.q0 + j) * p.Hq + h) * p.nsplit + blockIdx.x;
+    const int64_t at = (slot0 + row0 + row) * p.nsplit + blockIdx.x;
     p.po[at * PD + i] = o;
     if (i == 0) p.ml[at] = make_float2(top, l);
   }
 }
 
 // ---- queries into the rotated domain --------------------------------------------------------------------
-// q' = Pi q of four rows per block (thread = coordinate), stored as fp16 times a power of two that brings
+// q' = Pi q of a row block (thread = coordinate), stored as fp16 times a power of two that brings
 // the largest coordinate of the row into [2^11, 2^12): the rounding (2^-12 relative) is the only loss.
-constexpr int kPrepRows = 4;
+constexpr int kPrepRows = kRows;
 template <int D>
 __global__ void __launch_bounds__(D) prep_kernel(const __grid_constant__ PagedAttendParams p) {
   __shared__ float4 sq[kPrepRows][D / 4];
   __shared__ float red[kPrepRows][D / 32];
   const int i = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * kPrepRows, rows = p.total_q * p.Hq;
+  const int b = blockIdx.y / p.Hkv, hkv = blockIdx.y % p.Hkv;
+  const PagedSeq sq_ = paged_seq(p, b);
+  const int row0 = blockIdx.x * kPrepRows, rows = sq_.qn * p.g;
+  if (row0 >= rows || rows > p.chunk_rows) return;
 #pragma unroll
   for (int u = 0; u < kPrepRows; ++u) {
-    const int64_t row = row0 + u, tok = row / p.Hq;
-    ((float*)sq[u])[i] =
-        row < rows ? __uint_as_float((uint32_t)p.q[tok * p.q_stride + (row - tok * p.Hq) * D + i] << 16) : 0.f;
+    const int row = min(row0 + u, rows - 1), j = row / p.g;
+    ((float*)sq[u])[i] = __uint_as_float(
+        (uint32_t)p.q[(int64_t)(sq_.q0 + j) * p.q_stride + (int64_t)(hkv * p.g + row - j * p.g) * D + i] << 16);
   }
   __syncthreads();
   float acc[kPrepRows] = {};
@@ -510,14 +478,15 @@ __global__ void __launch_bounds__(D) prep_kernel(const __grid_constant__ PagedAt
 #pragma unroll
   for (int u = 0; u < kPrepRows; ++u) {
     if (row0 + u >= rows) break;
+    const int64_t at = (int64_t)blockIdx.y * p.row_slots + row0 + u;
     float m = red[u][0];
 #pragma unroll
     for (int w = 1; w < D / 32; ++w) m = fmaxf(m, red[u][w]);
     // exponent field of the largest coordinate, kept where both 2^e and 2^-e are normal numbers
     const int e = min(max((__float_as_int(m) >> 23) & 255, 20), 230);
     const float up = __int_as_float((254 + 11 - e) << 23), down = __int_as_float((e - 11) << 23);
-    p.qr[(row0 + u) * D + i] = __float2half_rn(acc[u] * up);
-    if (i == 0) p.qs[row0 + u] = down;
+    p.qr[at * D + i] = __float2half_rn(acc[u] * up);
+    if (i == 0) p.qs[at] = down;
   }
 }
 
@@ -528,32 +497,34 @@ template <int D, bool ALG2>
 __global__ void __launch_bounds__(D) combine_kernel(const __grid_constant__ PagedAttendParams p) {
   constexpr int PD = ALG2 ? 2 * D : D;
   __shared__ float so[kCombRows][PD];
-  __shared__ int skip[kCombRows];
   const int i = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * kCombRows;
-  const int64_t used = min((int64_t)max(p.q_start[p.B], 0), p.total_q) * p.Hq;
-  if (row0 >= used) return;
-#pragma unroll 1
+  const int b = blockIdx.y / p.Hkv, hkv = blockIdx.y % p.Hkv;
+  const PagedSeq sq = paged_seq(p, b);
+  const int row0 = blockIdx.x * kCombRows, rows = sq.qn * p.g;
+  if (row0 >= rows || rows > p.chunk_rows) return;
+  int64_t at[kCombRows];
+#pragma unroll
   for (int u = 0; u < kCombRows; ++u) {
-    const int64_t row = row0 + u;
-    float c = 0.f, z = 0.f, l = 0.f;
-    if (row < used) {
-      const float2* ml = p.ml + row * p.nsplit;
-      const float* po = p.po + row * p.nsplit * PD;
-      float top = -INFINITY;
-      for (int s = 0; s < p.nsplit; ++s) top = fmaxf(top, ml[s].x);
-      if (top == -INFINITY) top = 0.f;
-      for (int s = 0; s < p.nsplit; ++s) {
-        const float f = ex2_approx(ml[s].x - top);
-        l = fmaf(f, ml[s].y, l);
-        c = fmaf(f, po[s * PD + i], c);
-        if (ALG2) z = fmaf(f, po[s * PD + D + i], z);
-      }
+    const int row = min(row0 + u, rows - 1), j = row / p.g;
+    at[u] = (int64_t)(sq.q0 + j) * p.Hq + hkv * p.g + row - j * p.g;
+  }
+#pragma unroll
+  for (int u = 0; u < kCombRows; ++u) {
+    const int64_t slot = ((int64_t)blockIdx.y * p.row_slots + min(row0 + u, rows - 1)) * p.nsplit;
+    const float2* ml = p.ml + slot;
+    const float* po = p.po + slot * PD;
+    float c = 0.f, z = 0.f, l = 0.f, top = -INFINITY;
+    for (int s = 0; s < p.nsplit; ++s) top = fmaxf(top, ml[s].x);
+    if (top == -INFINITY) top = 0.f;
+    for (int s = 0; s < p.nsplit; ++s) {
+      const float f = ex2_approx(ml[s].x - top);
+      l = fmaf(f, ml[s].y, l);
+      c = fmaf(f, po[s * PD + i], c);
+      if (ALG2) z = fmaf(f, po[s * PD + D + i], z);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;   // NaN stays NaN
     so[u][i] = c * inv;
     if (ALG2) so[u][D + i] = p.alpha * z * inv;
-    if (i == 0) skip[u] = row >= used;
   }
   __syncthreads();
   float acc[kCombRows] = {};
@@ -569,10 +540,7 @@ __global__ void __launch_bounds__(D) combine_kernel(const __grid_constant__ Page
   }
 #pragma unroll
   for (int u = 0; u < kCombRows; ++u)
-    if (!skip[u]) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(acc[u]);
-      p.out[(row0 + u) * D + i] = __bfloat16_as_ushort(h);
-    }
+    if (row0 + u < rows) p.out[at[u] * D + i] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[u]));
 }
 
 // ---- host -----------------------------------------------------------------------------------------------
@@ -580,26 +548,33 @@ __global__ void __launch_bounds__(D) combine_kernel(const __grid_constant__ Page
 struct Plan {
   int row_blocks, nsplit, span;
   size_t qr, qs, ml, po, total;
+  PagedChunkPlan chunk;
 };
 
-Plan plan(const tq_paged_kv* kv, int B, int Hq, int64_t total_q, int max_q, int64_t max_kv, int64_t max_seen) {
+Plan plan(const tq_paged_kv* kv, int B, int Hq, int64_t total_q, int max_q, int64_t max_kv, int window) {   // B and max_q > 0
   Plan P{};
   const int g = Hq / kv->Hkv;
-  P.row_blocks = (int)(((int64_t)max_q * g + kRows - 1) / kRows);
+  const bool chunks = (int64_t)max_q * g > kChunkRows;
+  P.row_blocks = chunks ? (kChunkRows + kRows - 1) / kRows : (max_q * g + kRows - 1) / kRows;
   // about four CTAs per resident slot (two per SM) where the tokens allow it, at least 256 tokens each
-  const int64_t units = (int64_t)std::max(B, 1) * kv->Hkv * std::max(P.row_blocks, 1);
+  const int64_t units = (int64_t)B * kv->Hkv * P.row_blocks;
   const int64_t most = std::max<int64_t>(1, (max_kv + 255) / 256);
   P.nsplit = (int)std::min<int64_t>({most, std::max<int64_t>(1, 148 * 8 / units), 128});
-  int64_t span = (std::min(max_seen, max_kv) + 15 + P.nsplit - 1) / P.nsplit;
+  // with a window (and no prefix) a row block sees the window and its own queries' span
+  int64_t seen = max_kv;
+  if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + (kRows + g - 1) / g + 1);
+  int64_t span = (seen + 15 + P.nsplit - 1) / P.nsplit;
   P.span = (int)((span + 15) / 16 * 16);
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = (size_t)total_q * Hq, pd = (size_t)kv->d * (kv->v_alg == 2 ? 2 : 1);
+  const size_t rows = (size_t)B * kv->Hkv * P.row_blocks * kRows, pd = (size_t)kv->d * (kv->v_alg == 2 ? 2 : 1);
   size_t off = 0;
   P.qr = off; off += al(rows * kv->d * 2);
   P.qs = off; off += al(rows * 4);
   P.ml = off; off += al(rows * P.nsplit * 8);
   P.po = off; off += al(rows * P.nsplit * pd * 4);
-  P.total = off;
+  P.chunk = chunks ? paged_chunk_plan(kv, B, Hq, total_q, max_q, max_kv, window) : PagedChunkPlan{};
+  P.chunk.base = off;
+  P.total = off + P.chunk.bytes;
   return P;
 }
 
@@ -656,7 +631,7 @@ tq_status check_sizes(const std::string& f, const tq_paged_kv* kv, int32_t B, in
   if (max_kv > ((int64_t)1 << 31) - 1024) return fail(TQ_ERR_UNSUPPORTED, f + ": max_kv_len too large");
   if (total_q > ((int64_t)1 << 31) - 1024 || total_q * Hq > ((int64_t)1 << 33))
     return fail(TQ_ERR_UNSUPPORTED, f + ": too many query rows for one call");
-  if (((int64_t)max_q * (Hq / kv->Hkv) + kRows - 1) / kRows > 65535)
+  if ((int64_t)max_q * (Hq / kv->Hkv) > 65535LL * 256)
     return fail(TQ_ERR_UNSUPPORTED, f + ": max_q_len too large for one call");
   return TQ_OK;
 }
@@ -669,7 +644,8 @@ using namespace tq;
 extern "C" TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, int32_t Hq, int64_t total_q,
                                                          int32_t max_q_len, int64_t max_kv_len) {
   if (check_sizes("tq_paged_attend_workspace_bytes", kv, B, Hq, total_q, max_q_len, max_kv_len) != TQ_OK) return 0;
-  return plan(kv, B, Hq, total_q, max_q_len, max_kv_len, max_kv_len).total;
+  if (B == 0 || total_q == 0 || max_q_len == 0) return 0;
+  return plan(kv, B, Hq, total_q, max_q_len, max_kv_len, 0).total;
 }
 
 extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, int32_t Hq, int64_t total_q,
@@ -695,10 +671,7 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
     return fail(TQ_ERR_INVALID_ARG, f + ": int32 / fp32 arrays must be 4-byte aligned");
   if (!work) return TQ_OK;
   const int g = Hq / kv->Hkv;
-  // with a window (and no prefix) a row block sees the window and its own queries' span
-  int64_t seen = max_kv_len;
-  if (window > 0 && !prefix_len) seen = std::min<int64_t>(seen, (int64_t)window + (kRows + g - 1) / g + 1);
-  const Plan P = plan(kv, B, Hq, total_q, max_q_len, max_kv_len, seen);
+  const Plan P = plan(kv, B, Hq, total_q, max_q_len, max_kv_len, prefix_len ? 0 : window);
   if (!ws || ws_bytes < tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len))
     return fail(TQ_ERR_WORKSPACE, f + ": workspace too small");
   if (!(scale > 0.0f)) scale = (float)(1.0 / std::sqrt((double)kv->d));
@@ -733,6 +706,9 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   p.cap2x = softcap > 0.0f ? 2.0f / softcap : 0.0f;   // x arrives times log2(e), as exp2 wants it
   p.v_inv_unit = 1.0f / kv->v_unit;
   p.alpha = (float)(std::sqrt(std::acos(-1.0) / 2.0) / kv->d);
+  p.k_unit = kv->k_unit;
+  p.k_inv_unit = 1.0f / kv->k_unit;
+  p.sign_unit = p.alpha * kv->v_unit;
   level_table(kv->k_half, kv->k_bits, p.ktab);
   level_table(kv->v_half, kv->v_bits, p.vtab);
   const RotLayout RL = rot_layout(kv->d);
@@ -748,24 +724,29 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   p.po = (float*)(w + P.po);
   p.nsplit = P.nsplit;
   p.span = P.span;
+  p.chunk_rows = kChunkRows;
+  p.row_slots = P.row_blocks * kRows;
   p.err = device_error_word();
   if (!p.err) return fail(TQ_ERR_CUDA, f + ": no device error word (is a CUDA device present?)");
   cudaStream_t st = (cudaStream_t)stream;
   const bool alg2 = kv->v_alg == 2;
-  const int64_t rows = total_q * Hq;
-  const unsigned pb = (unsigned)((rows + kPrepRows - 1) / kPrepRows), cb = (unsigned)((rows + kCombRows - 1) / kCombRows);
-  const dim3 grid(P.nsplit, P.row_blocks, B * kv->Hkv);
+  const dim3 grid(P.nsplit, P.row_blocks, B * kv->Hkv), pg(P.row_blocks, B * kv->Hkv),
+      cg(P.row_blocks * (kRows / kCombRows), B * kv->Hkv);
   cudaError_t e;
+  if (P.chunk.slots) {
+    s = paged_chunk_launch(p, kv, P.chunk, w + P.chunk.base, st);
+    if (s != TQ_OK) return s;
+  }
   if (kv->d == 128) {
-    prep_kernel<128><<<pb, 128, 0, st>>>(p);
+    prep_kernel<128><<<pg, 128, 0, st>>>(p);
     if ((s = launch_keys<128>(p, kv->k_bits, kv->v_bits, alg2, grid, st)) != TQ_OK) return s;
-    if (alg2) combine_kernel<128, true><<<cb, 128, 0, st>>>(p);
-    else combine_kernel<128, false><<<cb, 128, 0, st>>>(p);
+    if (alg2) combine_kernel<128, true><<<cg, 128, 0, st>>>(p);
+    else combine_kernel<128, false><<<cg, 128, 0, st>>>(p);
   } else {
-    prep_kernel<64><<<pb, 64, 0, st>>>(p);
+    prep_kernel<64><<<pg, 64, 0, st>>>(p);
     if ((s = launch_keys<64>(p, kv->k_bits, kv->v_bits, alg2, grid, st)) != TQ_OK) return s;
-    if (alg2) combine_kernel<64, true><<<cb, 64, 0, st>>>(p);
-    else combine_kernel<64, false><<<cb, 64, 0, st>>>(p);
+    if (alg2) combine_kernel<64, true><<<cg, 64, 0, st>>>(p);
+    else combine_kernel<64, false><<<cg, 64, 0, st>>>(p);
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tq_paged_attend: launch");
   return TQ_OK;

@@ -2,6 +2,7 @@
 #pragma once
 #include <cstdint>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 #include "sm100.cuh"
 
@@ -30,15 +31,19 @@ struct PagedAttendParams {
   float scale_log2;            // scale log2(e) / k_unit
   float cap2x, cap_log2;       // 2 / cap, cap log2(e) (cap = 0: none)
   float v_inv_unit, alpha;
+  float k_unit, k_inv_unit, sign_unit;   // chunk kernels: sign_unit = alpha times the values' unit
   uint32_t ktab[4], vtab[4];   // level tables for byte permutes: low bytes of levels 0-3, 4-7, high bytes
   const float* Pi;
   const float* S;
   const uint8_t* img[6];       // Pi_hi, Pi_lo, PiT_hi, PiT_lo, ST_hi, ST_lo shared-memory images
-  __half* qr;                  // rotated queries [total_q * Hq][d], scaled by a power of two per row
-  float* qs;                   // that scale's inverse [total_q * Hq]
-  float2* ml;                  // partial (reference, sum) [total_q * Hq][nsplit]
-  float* po;                   // partial outputs [total_q * Hq][nsplit][parts d]
+  // row r of unit b Hkv + hkv is workspace row unit * row_slots + r
+  int row_slots;
+  __half* qr;                  // rotated queries [rows][d], scaled by a power of two per row
+  float* qs;                   // that scale's inverse [rows]
+  float2* ml;                  // partial (reference, sum) [rows][nsplit]
+  float* po;                   // partial outputs [rows][nsplit][parts d]
   int nsplit, span;            // splits of the visible tokens, tokens of each
+  int chunk_rows;              // a sequence with more query rows per KV head takes the chunk kernels
   uint32_t* err;
 };
 
@@ -47,6 +52,20 @@ struct PagedSeq {
   int q0, qn;                  // first query row, number of queries
   int64_t kv;                  // filled slots
 };
+
+// The chunk kernels (paged_chunk.cu): their share of the workspace, and the launch.
+// Rows per KV head from which a sequence takes them: see paged_chunk.cu.
+constexpr int kChunkRows = 48;
+struct PagedChunkPlan {
+  int slots;                   // sequences that may have so many rows (0: none)
+  int group;                   // (sequence, KV head) units opened at a time
+  int tiles;                   // 128-token tiles of a unit, at most
+  int row_blocks;
+  size_t list, images, heads, base, bytes;
+};
+PagedChunkPlan paged_chunk_plan(const tq_paged_kv* kv, int B, int Hq, int64_t total_q, int max_q, int64_t max_kv, int window);
+tq_status paged_chunk_launch(const PagedAttendParams& p, const tq_paged_kv* kv, const PagedChunkPlan& P, uint8_t* ws,
+                             cudaStream_t st);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b) {
@@ -76,6 +95,40 @@ __device__ __forceinline__ void paged_range(const PagedAttendParams& p, const Pa
   hi = min(s.kv, max(p1 + 1, prefix));
   lo = p.window > 0 && prefix <= 0 ? max((int64_t)0, p0 - p.window + 1) : 0;
   if (hi < lo) hi = lo;
+}
+
+// Level indices as nibbles: nibble n of the result = index of coordinate s + 4 n (n = 0..3 from a shift of 16 h
+// + s). For 16 levels the nibble is the magnitude's index and `neg` has bit 0 of nibble n set where the
+// level is negative.
+template <int BITS>
+__device__ __forceinline__ uint32_t pick(const uint32_t* w, int shift, uint32_t& neg) {
+  uint32_t x = 0;
+  if constexpr (BITS == 4) {
+    neg = (~w[3] >> shift) & 0x11111111u;
+    const uint32_t f = ~w[3];
+#pragma unroll
+    for (int b = 0; b < 3; ++b) x |= (((w[b] ^ f) >> shift) & 0x11111111u) << b;
+  } else {
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) x |= ((w[b] >> shift) & 0x11111111u) << b;
+    neg = 0;
+  }
+  return x;
+}
+// Four levels from the low four nibbles of `sel`: (0, 1) and (2, 3) as fp16 pairs.
+template <int BITS>
+__device__ __forceinline__ void look_up(uint32_t sel, uint32_t neg, const uint32_t (&tab)[4], uint32_t& p0, uint32_t& p1) {
+  uint32_t lb, hb;
+  if constexpr (BITS <= 2) {
+    lb = __byte_perm(tab[0], 0u, sel);
+    hb = __byte_perm(tab[2], 0u, sel);
+  } else {
+    lb = __byte_perm(tab[0], tab[1], sel);
+    hb = __byte_perm(tab[2], tab[3], sel);
+  }
+  if constexpr (BITS == 4) hb ^= __byte_perm(0x8000u, 0u, neg);
+  p0 = __byte_perm(lb, hb, 0x5140u);
+  p1 = __byte_perm(lb, hb, 0x7362u);
 }
 
 __device__ __forceinline__ float ex2_approx(float x) {

@@ -1,0 +1,810 @@
+// Attention of chunks (many query rows per KV head) over the paged packed cache: tq_paged_attend's path for
+// sequences with more than kChunkRows rows.
+//
+// Two kernels per group of (sequence, KV head) units:
+//   open   decodes each 128-token tile once, K = n Pi^T c[idx] and V = n (Pi^T c[idx] + alpha gamma S^T (2 z - 1)),
+//          by tensor-core products with the prepared Pi^T and S^T images, into fp16 tiles that are already the
+//          shared-memory operands of the second kernel (K as [token][coordinate], V as [coordinate][token], both
+//          K-major with the 128-byte swizzle);
+//   chunk  out = softmax(scale q K^T, capped, biased, masked) V: tcgen05 products, 256 query rows per CTA.
+// A chunk of 2048 queries reads every tile 32 times (four heads per KV head), so that unpacking inside the
+// attention would cost more than the products; opened once, a tile is 64 KB that stay in L2 between its uses, and
+// values of Algorithm 2 take one product instead of two. Query rows need no rotation, outputs neither.
+//
+// fp16 holds a tile because each tile has a power of two of its own for keys and for values (its largest norm):
+// the keys' goes into the score factor. The values' exponent e is added to the scores of the softmax
+// numerators, P = 2^(x + e - M) with the running reference M over x + e, and taken out of the denominators
+// (2^-e sum P): no extra work per element, and P is rounded relative to what a row adds up.
+//
+// A record with a norm or residual norm that is not finite makes the rows that see it NaN; the tile holds zeros in
+// its place, so that no other row meets it.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "paged_attend.h"
+#include "sm100.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+constexpr int kTile = 128;            // tokens of a tile
+constexpr int kCtaRows = 256;         // query rows of a CTA: two groups of 128
+constexpr float kLazy = 8.0f;         // how far (log2) a score may pass the reference before it moves
+constexpr int kBits = 12;             // operands: norms below 1 after the tile's exponent, times 2^kBits
+
+// What the attention needs to know of a tile besides its operands.
+struct TileHead {
+  float k_unit;                       // score = factor * k_unit * <q, K>
+  float v_exp;                        // e
+  float v_unit;                       // 2^-e
+  uint32_t flags;                     // 1: some token is absent, 2: some token is not finite
+  uint32_t present[4];                // bit per token
+  uint32_t strange[4];                // bit per token: present, norm not finite
+  uint32_t pad[4];
+};
+static_assert(sizeof(TileHead) == 64, "tile head");
+
+struct ChunkParams {
+  const int32_t* list;                // [0] count, then the sequences that take this path
+  uint8_t* images;                    // [group][tiles][K, V][256 D bytes]
+  TileHead* heads;                    // [group][tiles]
+  int unit0, units, tiles;            // first unit of the group, units of the group, tiles of a unit
+};
+
+// Sequences with more than chunk_rows rows per KV head, in order.
+__global__ void __launch_bounds__(256) list_kernel(const __grid_constant__ PagedAttendParams p, int32_t* list, int most) {
+  __shared__ int warp_sum[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 256) {
+    const int b = b0 + threadIdx.x;
+    bool on = false;
+    if (b < p.B) {
+      const int q0 = p.q_start[b], q1 = p.q_start[b + 1];
+      on = q0 >= 0 && q1 >= q0 && q1 <= p.total_q && q1 - q0 <= p.max_q && (int64_t)(q1 - q0) * p.g > p.chunk_rows;
+    }
+    const uint32_t vote = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) warp_sum[warp] = __popc(vote);
+    __syncthreads();
+    int at = base, all = 0;
+    for (int w = 0; w < 8; ++w) {
+      at += w < warp ? warp_sum[w] : 0;
+      all += warp_sum[w];
+    }
+    at += __popc(vote & ((1u << lane) - 1));
+    if (on && at < most) list[1 + at] = b;
+    base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) list[0] = min(base, most);
+}
+
+// One unit of the launch: its sequence and what its queries may see between them.
+struct Unit {
+  int b, hkv;
+  PagedSeq sq;
+  int64_t first, prefix, lo, hi;      // position of query 0; visible tokens [lo, hi)
+};
+__device__ __forceinline__ bool find_unit(const PagedAttendParams& p, const ChunkParams& c, int u, Unit& x) {
+  const int slot = (c.unit0 + u) / p.Hkv;
+  if (slot >= c.list[0]) return false;
+  x.hkv = (c.unit0 + u) - slot * p.Hkv;
+  x.b = c.list[1 + slot];
+  x.sq = paged_seq(p, x.b);
+  x.first = x.sq.kv - x.sq.qn;
+  x.prefix = p.prefix ? min((int64_t)p.prefix[x.b], x.sq.kv) : 0;
+  paged_range(p, x.sq, x.first, x.first + x.sq.qn - 1, x.prefix, x.lo, x.hi);
+  return true;
+}
+
+// ---- open -----------------------------------------------------------------------------------------------
+template <int D, bool ALG2>
+struct OpenLayout {
+  static constexpr uint32_t kImg = 128 * D * 2, kMat = 0, kSgn = kImg, kK = kSgn + (ALG2 ? kImg : 0), kV = kK + kImg,
+                            kS = kV + kImg, kInfo = kS + (ALG2 ? kImg : 0), kBar = kInfo + 2 * 128 * 4 + 128,
+                            kTotal = kBar + 64 + 1024;
+};
+constexpr int kOpenThreads = 512;
+
+template <int D, int KB, int VB, bool ALG2>
+__global__ void __launch_bounds__(kOpenThreads, 1)
+    open_kernel(const __grid_constant__ PagedAttendParams p, const __grid_constant__ ChunkParams c) {
+  using L = OpenLayout<D, ALG2>;
+  constexpr int G = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  float* info = (float*)(smem + L::kInfo);                       // [key factor, value factor][128]
+  int* top = (int*)(info + 2 * 128);                             // [16 warps][key, value] exponents
+  uint64_t* bar = (uint64_t*)(smem + L::kBar);                   // matrices loaded, products done
+  uint32_t* tmem_slot = (uint32_t*)(bar + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tk = *tmem_slot, tv = tk + 128;
+  if (tid == 0) {   // 128-row images; at d = 64 the first column block alone
+    mbar_arrive_expect_tx(&bar[0], (ALG2 ? 2u : 1u) * L::kImg);
+    bulk_g2s(smem + L::kMat, p.img[2], L::kImg, &bar[0]);
+    if (ALG2) bulk_g2s(smem + L::kSgn, p.img[4], L::kImg, &bar[0]);
+  }
+  uint32_t ktab[4], vtab[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ktab[i] = p.ktab[i], vtab[i] = p.vtab[i];
+
+  // this thread's (token, 32-coordinate group) of a tile, and its records
+  const int tok = tid / G, grp = tid % G;
+  const bool unpacker = tid < kTile * G;
+  uint32_t kw[KB], vw[VB], sw = 0;
+  uint16_t kn = 0, vn = 0, vg = 0;
+  bool present = false;
+  auto fetch = [&](int item) {
+    present = false;
+    kn = vn = vg = 0;
+    sw = 0;
+#pragma unroll
+    for (int i = 0; i < KB; ++i) kw[i] = 0;
+#pragma unroll
+    for (int i = 0; i < VB; ++i) vw[i] = 0;
+    const int u = item / c.tiles;
+    Unit x;
+    if (u >= c.units || !find_unit(p, c, u, x)) return false;
+    const int64_t t0 = (x.lo & ~(int64_t)(kTile - 1)) + (int64_t)(item - u * c.tiles) * kTile;
+    if (t0 >= x.hi) return false;
+    if (unpacker) {
+      const int64_t t = t0 + tok;
+      if (t < x.hi) {
+        const int64_t page = p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)];
+        if (page >= 0 && page < p.num_pages) {
+          const int64_t rec = ((page * p.Hkv + x.hkv) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+          present = true;
+#pragma unroll
+          for (int i = 0; i < KB; ++i) kw[i] = __ldg(p.k_codes + (rec * G + grp) * KB + i);
+#pragma unroll
+          for (int i = 0; i < VB; ++i) vw[i] = __ldg(p.v_codes + (rec * G + grp) * VB + i);
+          kn = __ldg(p.k_norms + rec);
+          vn = __ldg(p.v_norms + rec);
+          if (ALG2) {
+            sw = __ldg(p.v_signs + rec * G + grp);
+            vg = __ldg(p.v_gammas + rec);
+          }
+        } else if (t >= x.lo) {
+          atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+        }
+      }
+    }
+    return true;
+  };
+
+  const int items = c.units * c.tiles;
+  int item = blockIdx.x;
+  bool live = item < items && fetch(item);
+  uint32_t phase = 0;
+  bool loaded = false;
+  while (item < items) {
+    if (!live) {                                                 // uniform over the block
+      item += gridDim.x;
+      live = item < items && fetch(item);
+      continue;
+    }
+    // ---- norms: factors of the tokens, exponents of the tile -------------------------------------------
+    const float fk = __half2float(__ushort_as_half(kn)), fv = __half2float(__ushort_as_half(vn));
+    const float fg = ALG2 ? __half2float(__ushort_as_half(vg)) : 0.f;
+    const bool fine = fabsf(fk) < INFINITY && fabsf(fv) < INFINITY && fabsf(fg) < INFINITY;
+    const float reach = fabsf(fv) * fmaxf(1.f, fabsf(fg));
+    __shared__ uint32_t words[2][4];
+    {
+      // exponent fields (of positive floats these order like the values); a token's G threads agree
+      int ek = fine ? (__float_as_int(fabsf(fk)) >> 23) : 0, ev = fine ? (__float_as_int(reach) >> 23) : 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        ek = max(ek, __shfl_xor_sync(0xffffffffu, ek, o));
+        ev = max(ev, __shfl_xor_sync(0xffffffffu, ev, o));
+      }
+      if (tid < 8) words[tid >> 2][tid & 3] = 0;
+      if (tid == 0) bulk_wait_read0();                           // the images' last copy has left shared memory
+      __syncthreads();
+      if (lane == 0 && unpacker) {
+        top[2 * warp] = ek;
+        top[2 * warp + 1] = ev;
+      }
+      if (unpacker && grp == 0) {
+        if (present) atomicOr(&words[0][tok >> 5], 1u << (tok & 31));
+        if (present && !fine) atomicOr(&words[1][tok >> 5], 1u << (tok & 31));
+      }
+    }
+    __syncthreads();
+    int ek = 0, ev = 0;
+    for (int w = 0; w < kTile * G / 32; ++w) {
+      ek = max(ek, top[2 * w]);
+      ev = max(ev, top[2 * w + 1]);
+    }
+    // norms times 2^-(e - 127 + 1) are below 1 (an empty tile: any exponent will do)
+    ek = ek == 0 ? 0 : ek - 126;
+    ev = ev == 0 ? 0 : ev - 126;
+    if (unpacker && grp == 0) {
+      const bool use = present && fine;
+      info[tok] = use ? ldexpf(fk, kBits - ek) * p.k_inv_unit : 0.f;
+      info[128 + tok] = use ? ldexpf(fv, kBits - ev) * p.v_inv_unit : 0.f;
+    }
+    if (tid == 0) {
+      TileHead* h = c.heads + item;
+      const bool all = (words[0][0] & words[0][1] & words[0][2] & words[0][3]) == 0xffffffffu;
+      const bool odd = (words[1][0] | words[1][1] | words[1][2] | words[1][3]) != 0;
+      h->k_unit = ldexpf(1.f, ek - kBits);
+      h->v_exp = (float)ev;
+      h->v_unit = ldexpf(1.f, -ev);
+      h->flags = (all ? 0u : 1u) | (odd ? 2u : 0u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h->present[i] = words[0][i], h->strange[i] = words[1][i];
+    }
+    // ---- unpack into operands ---------------------------------------------------------------------------
+    if (unpacker) {
+      uint32_t sg_lo = 0, sg_hi = 0;
+      if (ALG2) {   // alpha gamma in units of the levels, with either sign, as byte tables (z = 0: negative)
+        const uint32_t h = __half_as_ushort(__float2half_rn(present && fine ? p.sign_unit * fg : 0.f));
+        sg_lo = (h & 255u) * 0x0101u;
+        sg_hi = ((h >> 8) ^ 0x80u) | ((h >> 8) << 8);
+      }
+#pragma unroll
+      for (int s4 = 0; s4 < 4; ++s4) {
+        uint32_t nk, nv;
+        const uint32_t xk = pick<KB>(kw, s4, nk), xv = pick<VB>(vw, s4, nv);
+        uint32_t a[4], b[4];
+        look_up<KB>(xk, nk, ktab, a[0], a[1]);
+        look_up<KB>(xk >> 16, nk >> 16, ktab, a[2], a[3]);
+        look_up<VB>(xv, nv, vtab, b[0], b[1]);
+        look_up<VB>(xv >> 16, nv >> 16, vtab, b[2], b[3]);
+        const uint32_t off = sw128_offset(tok, (grp * 32 + s4 * 8) * 2, 128);
+        *(uint4*)(smem + L::kK + off) = make_uint4(a[0], a[1], a[2], a[3]);
+        *(uint4*)(smem + L::kV + off) = make_uint4(b[0], b[1], b[2], b[3]);
+        if (ALG2) {
+          const uint32_t z = (sw >> s4) & 0x11111111u;
+          uint32_t o[4];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t lb = __byte_perm(sg_lo, 0u, z >> (16 * half)), hb = __byte_perm(sg_hi, 0u, z >> (16 * half));
+            o[2 * half] = __byte_perm(lb, hb, 0x5140u);
+            o[2 * half + 1] = __byte_perm(lb, hb, 0x7362u);
+          }
+          *(uint4*)(smem + L::kS + off) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (!loaded) {
+      if (!__syncthreads_and(mbar_wait(&bar[0], 0, p.err, kDevTimeoutLoad, abort_flag))) break;
+      loaded = true;
+    }
+    tc_fence_after();
+    if (warp == 0 && elect_one_sync()) {
+      const uint32_t m = smem_u32(smem + L::kMat), sg = smem_u32(smem + L::kSgn), k = smem_u32(smem + L::kK),
+                     v = smem_u32(smem + L::kV), s = smem_u32(smem + L::kS);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
+        mma_f16_ss(tk, desc_kmajor_sw128(k + at), desc_kmajor_sw128(m + at), idesc_f16_f32(128, D), ks > 0);
+        mma_f16_ss(tv, desc_kmajor_sw128(m + at), desc_kmajor_sw128(v + at), idesc_f16_f32(128, 128), ks > 0);
+        if (ALG2) mma_f16_ss(tv, desc_kmajor_sw128(sg + at), desc_kmajor_sw128(s + at), idesc_f16_f32(128, 128), 1);
+      }
+      mma_commit(&bar[1]);
+    }
+    __syncwarp();
+    const int done = item;
+    item += gridDim.x;
+    live = item < items && fetch(item);
+    if (!__syncthreads_and(mbar_wait(&bar[1], phase, p.err, kDevTimeoutMma, abort_flag))) break;
+    phase ^= 1;
+    tc_fence_after();
+    // ---- products into fp16 tiles, in place of the operands -----------------------------------------------
+    const int quarter = warp & 3, part = warp >> 2;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    {
+      constexpr int W = D / 4;                                   // columns of a warp
+      const int row = quarter * 32 + lane;
+      const float f = info[row];
+#pragma unroll
+      for (int c0 = 0; c0 < W; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(tk + lane_base + part * W + c0, r);
+        tmem_ld_wait();
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __half2 x = __floats2half2_rn(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
+          h[i] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *(uint4*)(smem + L::kK + sw128_offset(row, (part * W + c0 + 8 * i) * 2, 128)) =
+              make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+      }
+    }
+    if (quarter * 32 < D) {
+      const int row = quarter * 32 + lane;
+#pragma unroll
+      for (int c0 = 0; c0 < 32; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(tv + lane_base + part * 32 + c0, r);
+        tmem_ld_wait();
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = *(const float4*)&info[128 + part * 32 + c0 + 4 * i];
+          const __half2 x = __floats2half2_rn(__uint_as_float(r[4 * i]) * f.x, __uint_as_float(r[4 * i + 1]) * f.y);
+          const __half2 y = __floats2half2_rn(__uint_as_float(r[4 * i + 2]) * f.z, __uint_as_float(r[4 * i + 3]) * f.w);
+          h[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+          h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *(uint4*)(smem + L::kV + sw128_offset(row, (part * 32 + c0 + 8 * i) * 2, D)) =
+              make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0) {
+      uint8_t* dst = c.images + (size_t)done * 2 * L::kImg;
+      bulk_s2g(dst, smem + L::kK, L::kImg);
+      bulk_s2g(dst + L::kImg, smem + L::kV, L::kImg);
+      bulk_commit();
+    }
+  }
+  if (tid == 0) {
+    if (!loaded) mbar_wait(&bar[0], 0, p.err, kDevTimeoutLoad, abort_flag);   // no copy outlives the block
+    bulk_wait0();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(*tmem_slot, 256);
+}
+
+// ---- chunk ----------------------------------------------------------------------------------------------
+// Warps 0-3 and 4-7: the softmax of query rows 0-127 and 128-255 (thread = row); warp 8 copies tiles; warp 9 owns
+// TMEM and issues the products. TMEM: scores S0, S1 (128 columns each; the weights P take the place of the
+// first 64 as fp16 pairs), outputs O0, O1 (D columns each).
+// The products run in the order S0 S1 | PV0 S0' | PV1 S1' | ..., so that one group's softmax overlaps the other
+// group's products. They complete in order: when a group's next scores are there, its PV product before them is
+// done, and the group may rescale its output in TMEM before it hands over the next weights.
+template <int D>
+struct ChunkLayout {
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr uint32_t kImg = 128 * D * 2, kQ = 0, kRing = 2 * kImg, kBar = kRing + kStages * kImg,
+                            kTotal = kBar + 256 + 1024;
+};
+constexpr int kChunkThreads = 320;
+constexpr int kChunkCols = 512;
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 pairs of A's K in a column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+enum CBars { Q_FULL = 0, KV_FULL = 2, KV_EMPTY = 10, S_FULL = 18, P_FULL = 20, O_FULL = 22, CNBARS = 24 };
+
+// bits [0, n) of the 32 columns from c0 on, where n counts from column 0 of the tile
+__device__ __forceinline__ uint32_t below(int64_t n, int c0) {
+  const int64_t k = n - c0;
+  return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_kernel(const __grid_constant__ PagedAttendParams p, const __grid_constant__ ChunkParams c) {
+  using L = ChunkLayout<D>;
+  constexpr int NS = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* bar = (uint64_t*)(smem + L::kBar);
+  uint32_t* tmem_slot = (uint32_t*)(bar + CNBARS);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Unit x;
+  if (!find_unit(p, c, blockIdx.x, x)) return;
+  const int rows = x.sq.qn * p.g, row0 = (gridDim.y - 1 - blockIdx.y) * kCtaRows;
+  if (row0 >= rows) return;
+  int64_t lo, hi;
+  paged_range(p, x.sq, x.first + row0 / p.g, x.first + (min(rows, row0 + kCtaRows) - 1) / p.g, x.prefix, lo, hi);
+  const int64_t unit_t0 = x.lo & ~(int64_t)(kTile - 1);
+  const int tile0 = (int)((lo - unit_t0) / kTile);
+  const int n = hi > lo ? (int)((hi - unit_t0 + kTile - 1) / kTile) - tile0 : 0;
+  const bool two = rows > row0 + 128;
+  const size_t item0 = (size_t)blockIdx.x * c.tiles + tile0;
+
+  if (tid == 0) {
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&bar[Q_FULL + u], 4);
+      mbar_init(&bar[S_FULL + u], 1);
+      mbar_init(&bar[P_FULL + u], 4);
+      mbar_init(&bar[O_FULL + u], 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bar[KV_FULL + s], 1);
+      mbar_init(&bar[KV_EMPTY + s], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, kChunkCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp == 8) {
+    if (elect_one_sync()) {
+      int k = 0;
+      for (; k < 2 * n; ++k) {                                   // K and V of tile k / 2 in turn
+        const int s = k % NS;
+        if (!mbar_wait(&bar[KV_EMPTY + s], ((k / NS) & 1) ^ 1, p.err, kDevTimeoutSync, abort_flag)) break;
+        mbar_arrive_expect_tx(&bar[KV_FULL + s], L::kImg);
+        bulk_g2s(smem + L::kRing + s * L::kImg, c.images + (2 * item0 + k) * L::kImg, L::kImg, &bar[KV_FULL + s]);
+      }
+      if (*abort_flag)                                           // no copy outlives the block
+        for (int i = max(0, k - NS); i < k; ++i) mbar_wait(&bar[KV_FULL + i % NS], (i / NS) & 1, nullptr, 0, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    const uint32_t ring = smem_u32(smem + L::kRing), q = smem_u32(smem + L::kQ);
+    const int groups = two ? 2 : 1;
+    auto scores = [&](int u, int k) {
+      if (elect_one_sync()) {
+        const uint32_t b = ring + (k % NS) * L::kImg;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
+          mma_f16_ss(tbase + 128 * u, desc_kmajor_sw128(q + u * L::kImg + at), desc_kmajor_sw128(b + at),
+                     idesc_f16_f32(128, 128), ks > 0);
+        }
+        mma_commit(&bar[S_FULL + u]);
+      }
+      __syncwarp();
+    };
+    auto free_stage = [&](int k) {
+      if (elect_one_sync()) mma_commit(&bar[KV_EMPTY + k % NS]);
+      __syncwarp();
+    };
+    auto wait = [&](int b, int ph, uint32_t code) {
+      const bool ok = mbar_wait_warp(&bar[b], ph & 1, p.err, code, abort_flag);
+      tc_fence_after();
+      return ok;
+    };
+    bool ok = n > 0 && wait(KV_FULL, 0, kDevTimeoutLoad);
+    for (int u = 0; ok && u < groups; ++u) {
+      ok = wait(Q_FULL + u, 0, kDevTimeoutSync);
+      if (ok) scores(u, 0);
+    }
+    if (ok) free_stage(0);
+    for (int j = 0; ok && j < n; ++j) {
+      const int kv = 2 * j + 1, kn = 2 * j + 2;                  // this tile's V, the next one's K
+      ok = wait(KV_FULL + kv % NS, kv / NS, kDevTimeoutLoad);
+      for (int u = 0; ok && u < groups; ++u) {
+        ok = wait(P_FULL + u, j, kDevTimeoutSync);
+        if (!ok) break;
+        if (elect_one_sync()) {
+          const uint32_t b = ring + (kv % NS) * L::kImg;
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_f16_ts(tbase + 256 + D * u, tbase + 128 * u + 8 * ks,
+                       desc_kmajor_sw128(b + (ks >> 2) * (D * 128u) + (ks & 3) * 32u), idesc_f16_f32(128, D),
+                       j > 0 || ks > 0);
+          if (j + 1 == n) mma_commit(&bar[O_FULL + u]);
+        }
+        __syncwarp();
+        if (j + 1 < n) {
+          if (u == 0) ok = wait(KV_FULL + kn % NS, kn / NS, kDevTimeoutLoad);
+          if (ok) scores(u, kn);
+        }
+      }
+      if (ok) free_stage(kv);
+      if (ok && j + 1 < n) free_stage(kn);
+    }
+  } else if (warp < 4 || two) {
+    const int u = warp >> 2, r = tid & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tbase + lane_base + 128 * u, to = tbase + lane_base + 256 + D * u;
+    const int row = row0 + 128 * u + r;
+    const bool on = row < rows;
+    const int jq = on ? row / p.g : 0, h = x.hkv * p.g + (on ? row - jq * p.g : 0);
+    const int64_t pos = x.first + jq;
+    // ---- this row's query: fp16 times a power of two (exact for what lies within 2^-26 of its largest) -----
+    float fac;
+    {
+      const uint4* src = (const uint4*)(p.q + (int64_t)(x.sq.q0 + jq) * p.q_stride + (int64_t)h * D);
+      uint4 w[D / 8];
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        w[i] = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = max(most, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
+      }
+      const int e = min(max((int)(most >> 7), 20), 230);
+      const float up = __int_as_float((254 + 11 - e) << 23);
+      fac = p.scale_log2 * p.k_unit * __int_as_float((e - 11) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 x2 = __floats2half2_rn(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+          o[k] = *reinterpret_cast<const uint32_t*>(&x2);
+        }
+        *(uint4*)(smem + L::kQ + u * L::kImg + sw128_offset(r, i * 16, 128)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[Q_FULL + u]);
+    }
+    const float slope = p.slopes ? p.slopes[h] * kLog2e : 0.f;
+    float ref = -INFINITY, sum = 0.f;
+    // the group's first and last position, for tiles that every row sees whole
+    const int64_t pmin = x.first + (row0 + 128 * u) / p.g, pmax = x.first + (min(rows, row0 + 128 * u + 128) - 1) / p.g;
+    const TileHead* heads = c.heads + item0;
+    int64_t t0 = unit_t0 + (int64_t)tile0 * kTile;
+    bool ok = true;
+    for (int j = 0; j < n; ++j, t0 += kTile) {
+      const float4 hd = *(const float4*)&heads[j];
+      const uint32_t flags = __float_as_uint(hd.w);
+      ok = mbar_wait_warp(&bar[S_FULL + u], j & 1, p.err, kDevTimeoutMma, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      float s[kTile];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+      tmem_ld_wait();
+      float f = fac * hd.x;
+      const bool whole = flags == 0 && ((t0 + kTile - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window)) || t0 + kTile <= x.prefix);
+      if (p.cap_log2 > 0.f || p.slopes || !whole) {
+        const float near = slope * (float)(t0 - pos);
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) s[i] *= f;
+        if (p.cap_log2 > 0.f) {
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) s[i] = capped(s[i] * p.cap2x, p.cap_log2);
+        }
+        if (p.slopes) {
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) s[i] += fmaf(slope, (float)i, near);
+        }
+        f = 1.f;
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // seen: present and ((t <= pos and t > pos - window) or t < prefix)
+            uint32_t m = below(pos + 1 - t0, 32 * i);
+            if (p.window > 0) m &= ~below(pos - p.window + 1 - t0, 32 * i);
+            m |= below(x.prefix - t0, 32 * i);
+            m = on ? m & __ldg(&heads[j].present[i]) : 0u;
+            const uint32_t strange = flags & 2u ? m & __ldg(&heads[j].strange[i]) : 0u;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              s[32 * i + k] = (m >> k) & 1 ? s[32 * i + k] : -INFINITY;
+              if (flags & 2u) s[32 * i + k] = (strange >> k) & 1 ? __int_as_float(0x7FC00000) : s[32 * i + k];
+            }
+          }
+        }
+      }
+      float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int i = 4; i < kTile; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+      const float top = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f, hd.y);
+      if (__any_sync(0xffffffffu, top > ref + kLazy)) {
+        const float nr = fmaxf(ref, top);
+        const float g = nr == ref ? 1.f : ex2_approx(ref - nr);  // 0 from the empty state
+        ref = nr;
+        sum *= g;
+        if (j > 0) {
+#pragma unroll
+          for (int i = 0; i < D; i += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + i, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
+            tmem_st16(to + i, o);
+          }
+        }
+      }
+      const float off = hd.y - (ref == -INFINITY ? 0.f : ref);
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kTile; i += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float a = ex2_approx(fmaf(s[i + 2 * k], f, off)), b = ex2_approx(fmaf(s[i + 2 * k + 1], f, off));
+          l4[(2 * k) & 3] += a;
+          l4[(2 * k + 1) & 3] += b;
+          const __half2 h2 = __floats2half2_rn(a, b);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        tmem_st16(ts + i / 2, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[P_FULL + u]);
+      sum = fmaf((l4[0] + l4[1]) + (l4[2] + l4[3]), hd.z, sum);
+    }
+    // ---- out = O / sum ------------------------------------------------------------------------------------
+    if (n > 0 && ok) ok = mbar_wait_warp(&bar[O_FULL + u], 0, p.err, kDevTimeoutMma, abort_flag);
+    if (ok) {
+      tc_fence_after();
+      const float inv = sum == 0.f ? 0.f : __int_as_float((127 - kBits) << 23) / sum;
+      uint4* dst = (uint4*)(p.out + ((int64_t)(x.sq.q0 + jq) * p.Hq + h) * D);
+#pragma unroll
+      for (int i = 0; i < D; i += 16) {
+        uint32_t o[16];
+        if (n > 0) {
+          tmem_ld16(to + i, o);
+          tmem_ld_wait();
+        }
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float a = sum == 0.f ? 0.f : __uint_as_float(o[2 * k]) * inv, b = sum == 0.f ? 0.f : __uint_as_float(o[2 * k + 1]) * inv;
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        if (on) {
+          dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[i / 8 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tbase, kChunkCols);
+}
+
+// ---- host -----------------------------------------------------------------------------------------------
+
+template <int D, int KB, int VB, bool ALG2>
+tq_status launch_open(const PagedAttendParams& p, const ChunkParams& c, cudaStream_t st) {
+  auto kern = open_kernel<D, KB, VB, ALG2>;
+  constexpr int smem = OpenLayout<D, ALG2>::kTotal;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "tq_paged_attend: shared memory attribute");
+  const int64_t items = (int64_t)c.units * c.tiles;
+  kern<<<(unsigned)std::min<int64_t>(items, sm_count()), kOpenThreads, smem, st>>>(p, c);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tq_paged_attend: launch");
+  return TQ_OK;
+}
+template <int D, int KB>
+tq_status launch_open_values(const PagedAttendParams& p, const ChunkParams& c, int vb, bool alg2, cudaStream_t st) {
+  if (alg2) switch (vb) {
+      case 1: return launch_open<D, KB, 1, true>(p, c, st);
+      case 2: return launch_open<D, KB, 2, true>(p, c, st);
+      default: return launch_open<D, KB, 3, true>(p, c, st);
+    }
+  switch (vb) {
+    case 1: return launch_open<D, KB, 1, false>(p, c, st);
+    case 2: return launch_open<D, KB, 2, false>(p, c, st);
+    case 3: return launch_open<D, KB, 3, false>(p, c, st);
+    default: return launch_open<D, KB, 4, false>(p, c, st);
+  }
+}
+template <int D>
+tq_status launch_unit_group(const PagedAttendParams& p, const ChunkParams& c, const tq_paged_kv* kv, int row_blocks, cudaStream_t st) {
+  const bool alg2 = kv->v_alg == 2;
+  tq_status s;
+  switch (kv->k_bits) {
+    case 1: s = launch_open_values<D, 1>(p, c, kv->v_bits, alg2, st); break;
+    case 2: s = launch_open_values<D, 2>(p, c, kv->v_bits, alg2, st); break;
+    case 3: s = launch_open_values<D, 3>(p, c, kv->v_bits, alg2, st); break;
+    default: s = launch_open_values<D, 4>(p, c, kv->v_bits, alg2, st);
+  }
+  if (s != TQ_OK) return s;
+  auto kern = chunk_kernel<D>;
+  constexpr int smem = ChunkLayout<D>::kTotal;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "tq_paged_attend: shared memory attribute");
+  kern<<<dim3(c.units, row_blocks), kChunkThreads, smem, st>>>(p, c);
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tq_paged_attend: launch");
+  return TQ_OK;
+}
+
+size_t tile_bytes(int d) { return (size_t)2 * 128 * d * 2; }
+
+}  // namespace
+
+// Opened tiles take 2 x 256 d bytes each, so a call opens its units in groups of at most this many bytes of tiles
+// (one unit at least).
+constexpr int64_t kOpenBytes = (int64_t)1 << 30;
+
+PagedChunkPlan paged_chunk_plan(const tq_paged_kv* kv, int B, int Hq, int64_t total_q, int max_q, int64_t max_kv, int window) {
+  PagedChunkPlan P{};
+  const int g = Hq / kv->Hkv;
+  P.slots = (int)std::min<int64_t>(B, total_q * g / (kChunkRows + 1));
+  if (max_kv == 0) max_kv = 1;
+  const int64_t units = std::max<int64_t>((int64_t)P.slots * kv->Hkv, 1), all = (max_kv + kTile - 1) / kTile;
+  const int64_t most = std::min<int64_t>(units, std::max<int64_t>(1, kOpenBytes / (all * (int64_t)tile_bytes(kv->d)))) * all;
+  // with a window a unit's queries see its span and their own; the tiles are then shared among more units
+  int64_t tiles = all;
+  if (window > 0) tiles = std::min<int64_t>(all, ((int64_t)window + max_q + kTile - 1) / kTile + 1);
+  P.tiles = (int)tiles;
+  P.group = (int)std::min<int64_t>(units, most / tiles);
+  P.row_blocks = (int)(((int64_t)max_q * g + kCtaRows - 1) / kCtaRows);
+  auto al = [](size_t v) { return (v + 255) / 256 * 256; };
+  size_t off = 0;
+  P.list = off; off += al((size_t)(P.slots + 1) * 4);
+  P.heads = off; off += al((size_t)most * sizeof(TileHead));
+  P.images = off; off += al((size_t)most * tile_bytes(kv->d));
+  P.bytes = off;
+  return P;
+}
+
+tq_status paged_chunk_launch(const PagedAttendParams& p, const tq_paged_kv* kv, const PagedChunkPlan& P, uint8_t* ws,
+                             cudaStream_t st) {
+  ChunkParams c{};
+  int32_t* list = (int32_t*)(ws + P.list);
+  c.list = list;
+  c.heads = (TileHead*)(ws + P.heads);
+  c.images = ws + P.images;
+  c.tiles = P.tiles;
+  list_kernel<<<1, 256, 0, st>>>(p, list, P.slots);
+  const int units = P.slots * kv->Hkv;
+  for (c.unit0 = 0; c.unit0 < units; c.unit0 += P.group) {
+    c.units = std::min(P.group, units - c.unit0);
+    const tq_status s = kv->d == 128 ? launch_unit_group<128>(p, c, kv, P.row_blocks, st)
+                                     : launch_unit_group<64>(p, c, kv, P.row_blocks, st);
+    if (s != TQ_OK) return s;
+  }
+  return TQ_OK;
+}
+
+}  // namespace tq

@@ -555,6 +555,15 @@ def test_attend_same_results_every_time(dev):
         pool.lens = kept
 
 
+def test_attend_opens_units_in_groups(dev):
+    """Limits so large that the chunks' tiles are opened one (sequence, KV head) at a time."""
+    pool = Paged(dev, [300, 190, 20], 2, 128, 3, 3, 2, 16, seed=2)
+    q = queries(np.random.default_rng(2), 221, 4, 128, dev)
+    pool.check(pool.call(q, [130, 90, 1], max_kv=1500000), q, [130, 90, 1])
+    pool.check(pool.call(q, [130, 90, 1], max_kv=1500000, window=77), q, [130, 90, 1], window=77)
+    tq.tq_sync_check()
+
+
 def test_attend_dirty_workspace_and_single_rows(dev):
     """A workspace of NaN bytes, one token, one query of one head."""
     pool = Paged(dev, [1, 3], 1, 64, 1, 2, 2, 16, seed=1)
