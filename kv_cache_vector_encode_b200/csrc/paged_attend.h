@@ -28,21 +28,23 @@ struct PagedAttendParams {
   const float* slopes;
   const uint16_t* q;           // bf16
   uint16_t* out;               // bf16
-  float scale_log2;            // scale log2(e) / k_unit
+  float scale_log2;            // scale log2(e)
+  float key_fac;               // scale_log2 times what a unit of the integer scores (over 256) is worth
   float cap2x, cap_log2;       // 2 / cap, cap log2(e) (cap = 0: none)
   float v_inv_unit, alpha;
-  float k_unit, k_inv_unit, sign_unit;   // chunk kernels: sign_unit = alpha times the values' unit
-  uint32_t ktab[4], vtab[4];   // level tables for byte permutes: low bytes of levels 0-3, 4-7, high bytes
+  float k_inv_unit, sign_unit; // chunk kernels: sign_unit = alpha times the values' unit
+  // level tables for byte permutes (low bytes of levels 0-3, 4-7, high bytes): fp16, and 16-bit integers
+  uint32_t ktab[4], vtab[4], klimb[4];
   const float* Pi;
   const float* S;
   const uint8_t* img[6];       // Pi_hi, Pi_lo, PiT_hi, PiT_lo, ST_hi, ST_lo shared-memory images
-  // row r of unit b Hkv + hkv is workspace row unit * row_slots + r
-  int row_slots;
-  __half* qr;                  // rotated queries [rows][d], scaled by a power of two per row
-  float* qs;                   // that scale's inverse [rows]
-  float2* ml;                  // partial (reference, sum) [rows][nsplit]
-  float* po;                   // partial outputs [rows][nsplit][parts d]
-  int nsplit, span;            // splits of the visible tokens, tokens of each
+  // decode steps: item (b Hkv + hkv) * row_blocks + rb holds rows_per_item query rows; see paged_rows.cuh
+  int row_blocks, rows_per_item;
+  int8_t* qr;                  // rotated queries [item][row][high, low limb][d], in the look-up's order
+  float2* qs;                  // (value of a unit, half the sum of the integers) [item][row]
+  int2* parts;                 // (first slot, number) of an item's partial results
+  float2* ml;                  // partial (reference, sum) [slot][row]
+  float* po;                   // partial outputs [slot][row][parts d]
   int chunk_rows;              // a sequence with more query rows per KV head takes the chunk kernels
   uint32_t* err;
 };
@@ -67,14 +69,34 @@ PagedChunkPlan paged_chunk_plan(const tq_paged_kv* kv, int B, int Hq, int64_t to
 tq_status paged_chunk_launch(const PagedAttendParams& p, const tq_paged_kv* kv, const PagedChunkPlan& P, uint8_t* ws,
                              cudaStream_t st);
 
+// The main kernel of decode steps, on `ctas` CTAs.
+tq_status paged_rows_launch_64(const PagedAttendParams& p, int kb, int vb, bool alg2, int ctas, cudaStream_t st);
+tq_status paged_rows_launch_128(const PagedAttendParams& p, int kb, int vb, bool alg2, int ctas, cudaStream_t st);
+
 #ifdef __CUDACC__
-__device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b) {
+// Launch of a kernel that waits for the one before it itself (griddepcontrol).
+inline cudaError_t launch_dependent(void (*kern)(PagedAttendParams), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                                    const PagedAttendParams& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+__device__ __forceinline__ PagedSeq paged_seq_checked(const PagedAttendParams& p, int b, bool& bad) {
   PagedSeq s;
   s.q0 = p.q_start[b];
   int q1 = p.q_start[b + 1];
   int64_t kv = p.kv_len[b];
   const int64_t most = min(p.max_kv, (int64_t)p.max_pages << p.page_shift);
-  bool bad = false;
+  bad = false;
   if (s.q0 < 0 || q1 < s.q0 || q1 > p.total_q || q1 - s.q0 > p.max_q) {
     bad = true;
     s.q0 = q1 = 0;
@@ -83,9 +105,18 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b)
     bad = true;
     kv = kv < 0 ? 0 : most;
   }
-  if (bad && threadIdx.x == 0) atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
   s.qn = q1 - s.q0;
   s.kv = kv;
+  return s;
+}
+__device__ __forceinline__ PagedSeq paged_seq_quiet(const PagedAttendParams& p, int b) {
+  bool bad;
+  return paged_seq_checked(p, b, bad);
+}
+__device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b) {
+  bool bad;
+  const PagedSeq s = paged_seq_checked(p, b, bad);
+  if (bad && threadIdx.x == 0) atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
   return s;
 }
 
@@ -97,6 +128,16 @@ __device__ __forceinline__ void paged_range(const PagedAttendParams& p, const Pa
   if (hi < lo) hi = lo;
 }
 
+// Index nibbles of coordinates s + 4 n (n = 0..7) of a 32-coordinate group, s known at compile time: a shift and
+// a masked merge per plane. For 16 levels w holds the magnitudes' planes.
+template <int BITS>
+__device__ __forceinline__ uint32_t nibbles(const uint32_t* w, int s) {
+  uint32_t x = 0;
+#pragma unroll
+  for (int b = 0; b < (BITS == 4 ? 3 : BITS); ++b)
+    x |= (s >= b ? w[b] >> (s - b) : w[b] << (b - s)) & (0x11111111u << b);
+  return x;
+}
 // Level indices as nibbles: nibble n of the result = index of coordinate s + 4 n (n = 0..3 from a shift of 16 h
 // + s). For 16 levels the nibble is the magnitude's index and `neg` has bit 0 of nibble n set where the
 // level is negative.

@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       const int e = min(max((int)(most >> 7), 20), 230);
       const float up = __int_as_float((254 + 11 - e) << 23);
-      fac = p.scale_log2 * p.k_unit * __int_as_float((e - 11) << 23);
+      fac = p.scale_log2 * __int_as_float((e - 11) << 23);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
