@@ -394,22 +394,64 @@ def tq_attend_append(cb_k: Codebook, cb_v: Codebook, q, rot, k_new, v_new, T_cur
 
 
 # ---- rotary positions, packed cache in pages -----------------------------------------------------
+# These are called once per layer and step, on few rows at a time, where the host's time is what a caller
+# waits for: the checks below use the cheapest accessors (get_device() tells device and kind at once).
 
-def _on(device, dtype, **tensors):
-    """Checks of the calls below: each tensor given is on `device`, contiguous and of `dtype`; the device is
-    the current one (the calls launch there)."""
-    for name, t in tensors.items():
-        if t is not None and (t.dtype is not dtype or t.device != device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+class _Torch:
+    """What the checks need of torch, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.f32, self.bf16, self.f16, self.i32, self.i64 = (torch.float32, torch.bfloat16, torch.float16, torch.int32,
+                                                             torch.int64)
+        self.code = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_tc = None
+
+
+def _torch() -> _Torch:
+    global _tc
+    if _tc is None:
+        lib()
+        _tc = _Torch()
+    return _tc
 
 
 def _current(t, name):
-    import torch
-    if not t.is_cuda:
+    """Index of the CUDA device that t is on, which has to be the current one (the calls launch there)."""
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if device != _torch().current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t.device
+    return device
+
+
+def _in(t, name, device, dtype, *shape):
+    """Address of a contiguous tensor of this device, dtype and shape."""
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on device {device}")
+    return t.data_ptr()
+
+
+def _table(table, device):
+    """Address, positions and rotated dimensions of a tq_rope_table."""
+    if table.get_device() != device or table.dtype is not _tc.f32 or table.dim() != 3 or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous torch.float32 tensor [n_pos, rot_dim // 2, 2] on device {device}")
+    n_pos, half, two = table.shape
+    if two != 2:
+        raise ValueError("table must be [n_pos, rot_dim // 2, 2]")
+    return table.data_ptr(), n_pos, 2 * half
+
+
+def _raw(stream, device):
+    if stream is None:
+        return _tc.raw_stream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def tq_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: int = TQ_ROPE_PLAIN, factor: float = 1.0,
@@ -429,24 +471,26 @@ def tq_rope(x, positions, table, out=None, layout: int = TQ_ROPE_HALF, inverse: 
     """Turns the heads of x [tokens, heads, d] (float32 / bfloat16 / float16, last axis contiguous) to positions
     [tokens] (int32; negative: a padding row, left as it is). out: x itself by default (in place).
     inverse=True turns the other way: the gradient with respect to x."""
-    import torch
     device = _current(x, "x")
-    if out is None:
-        out = x
-    if x.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    code = _tc.code.get(x.dtype)
+    if code is None:
         raise ValueError(f"x: dtype {x.dtype} not float32 / bfloat16 / float16")
     tokens, heads, d = x.shape
-    if out.shape != x.shape or out.dtype is not x.dtype or out.device != device:
-        raise ValueError("out must have the shape, dtype and device of x")
-    if x.stride(2) != 1 or out.stride(2) != 1:
+    xt, xh, xd = os_ = x.stride()
+    if out is None:
+        out = x
+    else:
+        if out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != device:
+            raise ValueError("out must have the shape, dtype and device of x")
+        os_ = out.stride()
+    if xd != 1 or os_[2] != 1:
         raise ValueError("the last axis of x and out must be contiguous")
-    _on(device, torch.int32, positions=positions)
-    _on(device, torch.float32, table=table)
-    if positions.shape != (tokens,) or table.dim() != 3 or table.shape[2] != 2:
-        raise ValueError("positions must be [tokens] and table [n_pos, rot_dim // 2, 2]")
-    _check(lib().tq_rope(tokens, heads, d, 2 * table.shape[1], layout, 1 if inverse else 0, x.data_ptr(), x.stride(0),
-                         x.stride(1), _xdtype(x), positions.data_ptr(), table.data_ptr(), table.shape[0],
-                         out.data_ptr(), out.stride(0), out.stride(1), _stream(stream)))
+    pos = _in(positions, "positions", device, _tc.i32, tokens)
+    tab, n_pos, rot_dim = _table(table, device)
+    status = _lib.tq_rope(tokens, heads, d, rot_dim, layout, 1 if inverse else 0, x.data_ptr(), xt, xh, code, pos, tab, n_pos,
+                          out.data_ptr(), os_[0], os_[1], _raw(stream, device))
+    if status:
+        _check(status)
     return out
 
 
@@ -456,8 +500,7 @@ class PagedKV:
     and v_gammas for values by Algorithm 2. It keeps the tensors alive."""
 
     def __init__(self, cb_k: Codebook, cb_v: Codebook, k_codes, k_norms, v_codes, v_norms, v_signs=None, v_gammas=None):
-        import torch
-        self.device = _current(k_codes, "k_codes")
+        self.device = device = _current(k_codes, "k_codes")
         if k_codes.dim() != 5:
             raise ValueError("k_codes must be [pages, Hkv, page_size, d/32, bits]")
         at, groups = tuple(k_codes.shape[:3]), k_codes.shape[3]
@@ -466,10 +509,8 @@ class PagedKV:
         for name, t, shape in (("k_codes", k_codes, (*at, groups, cb_k.bits)), ("v_codes", v_codes, (*at, groups, cb_v.bits)),
                                ("k_norms", k_norms, at), ("v_norms", v_norms, at), ("v_signs", v_signs, (*at, groups)),
                                ("v_gammas", v_gammas, at)):
-            if t is not None and tuple(t.shape) != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
-        _on(self.device, torch.int32, k_codes=k_codes, v_codes=v_codes, v_signs=v_signs)
-        _on(self.device, torch.float16, k_norms=k_norms, v_norms=v_norms, v_gammas=v_gammas)
+            if t is not None:
+                _in(t, name, device, _tc.i32 if len(shape) > 3 else _tc.f16, *shape)
         self.tensors = (k_codes, k_norms, v_codes, v_norms, v_signs, v_gammas)
         self.num_pages, self.Hkv, self.page_size = at
         self.d = 32 * groups
@@ -484,32 +525,40 @@ def tq_paged_append(kv: PagedKV, k_new, v_new, slots, rot, positions=None, table
                     stream=None):
     """Encodes k_new, v_new [tokens, Hkv, d] (float32 / bfloat16) into slots [tokens] (int64; negative: a padding
     row) of the cache, the keys turned to `positions` (int32) with `table` on the way where they are given."""
-    import torch
-    if kv.device.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {kv.device}, which is not the current device")
+    device = kv.device
+    if device != _tc.current_device():
+        raise ValueError(f"the cache is on device {device}, which is not the current one")
+    Hkv, d = kv.Hkv, kv.d
+    dtype = k_new.dtype
+    if dtype is not _tc.bf16 and dtype is not _tc.f32:
+        raise ValueError(f"k_new: dtype {dtype} not float32 / bfloat16")
     tokens = k_new.shape[0]
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.shape != (tokens, kv.Hkv, kv.d) or t.dtype is not k_new.dtype or t.device != kv.device:
-            raise ValueError(f"{name} must be [tokens, {kv.Hkv}, {kv.d}] on {kv.device}, both of one dtype")
-        if t.stride(2) != 1 or (kv.Hkv > 1 and t.stride(1) != kv.d):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if k_new.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"k_new: dtype {k_new.dtype} not float32 / bfloat16")
-    if (positions is None) != (table is None):
+    strides = []
+    for t in (k_new, v_new):
+        if t.shape != (tokens, Hkv, d) or t.dtype is not dtype or t.get_device() != device:
+            raise ValueError(f"k_new and v_new must be [tokens, {Hkv}, {d}] on device {device}, both of one dtype")
+        st, sh, sd = t.stride()
+        if sd != 1 or (sh != d and Hkv > 1):
+            raise ValueError("k_new and v_new: the heads of a token must be contiguous")
+        strides.append(st if tokens > 1 else Hkv * d)            # a single token may have any stride
+    at = _in(slots, "slots", device, _tc.i64, tokens)
+    pos = tab = None
+    n_pos = rot_dim = 0
+    if positions is not None and table is not None:
+        pos = _in(positions, "positions", device, _tc.i32, tokens)
+        tab, n_pos, rot_dim = _table(table, device)
+    elif positions is not None or table is not None:
         raise ValueError("positions and table go together")
-    _on(kv.device, torch.int64, slots=slots)
-    _on(kv.device, torch.int32, positions=positions)
-    _on(kv.device, torch.float32, table=table)
-    if slots.shape != (tokens,) or (positions is not None and positions.shape != (tokens,)):
-        raise ValueError("slots and positions must be [tokens]")
-    if table is not None and (table.dim() != 3 or table.shape[2] != 2):
-        raise ValueError("table must be [n_pos, rot_dim // 2, 2]")
-    row = kv.Hkv * kv.d                                  # a single token may have any stride
-    ks, vs = (t.stride(0) if tokens > 1 else row for t in (k_new, v_new))
-    _check(lib().tq_paged_append(kv.ref, tokens, k_new.data_ptr(), ks, v_new.data_ptr(), vs, _xdtype(k_new),
-                                 slots.data_ptr(), None if positions is None else positions.data_ptr(),
-                                 None if table is None else table.data_ptr(), 0 if table is None else table.shape[0],
-                                 0 if table is None else 2 * table.shape[1], layout, _ptr(rot, "rot"), _stream(stream)))
+    status = _lib.tq_paged_append(kv.ref, tokens, k_new.data_ptr(), strides[0], v_new.data_ptr(), strides[1], _tc.code[dtype],
+                                  at, pos, tab, n_pos, rot_dim, layout, _prepared(rot, device), _raw(stream, device))
+    if status:
+        _check(status)
+
+
+def _prepared(rot, device):
+    if rot.get_device() != device:
+        raise ValueError(f"rot must be on device {device}")
+    return rot.data_ptr()
 
 
 def tq_paged_attend_workspace_bytes(kv: PagedKV, B: int, Hq: int, total_q: int, max_q_len: int, max_kv_len: int) -> int:
@@ -521,37 +570,35 @@ def tq_paged_attend(kv: PagedKV, q, q_start, kv_len, page_table, rot, out, max_q
     """Attention of the newest tokens of B sequences over the paged cache: q [total_q, Hq, d] bfloat16 (token stride
     free), out the same, contiguous; q_start [B + 1], kv_len [B], page_table [B, max_pages], prefix_len [B] int32;
     slopes [Hq] float32."""
-    import torch
-    if kv.device.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {kv.device}, which is not the current device")
-    total_q, Hq, d = q.shape
-    if d != kv.d or q.dtype is not torch.bfloat16 or q.device != kv.device:
-        raise ValueError(f"q must be bfloat16 [total_q, Hq, {kv.d}] on {kv.device}")
-    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != d):
+    device = kv.device
+    if device != _tc.current_device():
+        raise ValueError(f"the cache is on device {device}, which is not the current one")
+    total_q, Hq, d = shape = q.shape
+    if d != kv.d or q.dtype is not _tc.bf16 or q.get_device() != device:
+        raise ValueError(f"q must be bfloat16 [total_q, Hq, {kv.d}] on device {device}")
+    qt, qh, qd = q.stride()
+    if qd != 1 or (qh != d and Hq > 1):
         raise ValueError("q: the heads of a token must be contiguous")
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    _on(kv.device, torch.bfloat16, out=out)
-    _on(kv.device, torch.int32, q_start=q_start, kv_len=kv_len, page_table=page_table, prefix_len=prefix_len)
-    _on(kv.device, torch.float32, slopes=slopes)
     B = kv_len.shape[0]
-    if q_start.shape != (B + 1,) or page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("q_start must be [B + 1], kv_len [B] and page_table [B, max_pages]")
-    if prefix_len is not None and prefix_len.shape != (B,):
-        raise ValueError("prefix_len must be [B]")
-    if slopes is not None and slopes.shape != (Hq,):
-        raise ValueError("slopes must be [Hq]")
+    max_pages = page_table.shape[1]
+    out_ptr = _in(out, "out", device, _tc.bf16, *shape)
+    i32 = _tc.i32
+    start = _in(q_start, "q_start", device, i32, B + 1)
+    lens = _in(kv_len, "kv_len", device, i32, B)
+    pages = _in(page_table, "page_table", device, i32, B, max_pages)
+    prefix = None if prefix_len is None else _in(prefix_len, "prefix_len", device, i32, B)
+    slope = None if slopes is None else _in(slopes, "slopes", device, _tc.f32, Hq)
     if ws is None:
+        import torch
         ws = torch.empty(max(tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len), 16),
                          dtype=torch.uint8, device=q.device)
-    elif ws.device != kv.device:
-        raise ValueError(f"ws must be on {kv.device}")
-    _check(lib().tq_paged_attend(kv.ref, B, Hq, total_q, max_q_len, max_kv_len, q.data_ptr(),
-                                 q.stride(0) if total_q > 1 else Hq * d, TQ_BF16, q_start.data_ptr(), kv_len.data_ptr(),
-                                 page_table.data_ptr(), page_table.shape[1], 0.0 if scale is None else float(scale),
-                                 float(softcap), window, None if prefix_len is None else prefix_len.data_ptr(),
-                                 None if slopes is None else slopes.data_ptr(), _ptr(rot, "rot"), out.data_ptr(),
-                                 _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream)))
+    elif ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on device {device}")
+    status = _lib.tq_paged_attend(kv.ref, B, Hq, total_q, max_q_len, max_kv_len, q.data_ptr(), qt if total_q > 1 else Hq * d,
+                                  TQ_BF16, start, lens, pages, max_pages, scale or 0.0, softcap, window, prefix, slope,
+                                  _prepared(rot, device), out_ptr, ws.data_ptr(), ws.nbytes, _raw(stream, device))
+    if status:
+        _check(status)
     return out
 
 

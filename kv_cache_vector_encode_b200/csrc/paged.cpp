@@ -79,6 +79,8 @@ extern "C" TQ_API tq_status tq_paged_kv_init(const tq_codebook* cb_k, const tq_c
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)))
     return fail(TQ_ERR_UNSUPPORTED, f + ": page_size must be a power of two in 16..1024");
   if (num_pages < 1 || num_pages > 2147483647LL) return fail(TQ_ERR_INVALID_ARG, f + ": num_pages must be in 1..2^31 - 1");
+  if (num_pages * Hkv > (((int64_t)1 << 32) - 1) / (page_size / 16))
+    return fail(TQ_ERR_UNSUPPORTED, f + ": more than 2^36 token slots over all KV heads");
   for (const tq_codebook* cb : {cb_k, cb_v}) {
     if (cb->d != d || cb->bits < 1 || cb->bits > 4 || cb->levels != (1 << cb->bits))
       return fail(TQ_ERR_INVALID_ARG, f + ": codebook does not match d / has bad bits");

@@ -213,7 +213,7 @@ Plan plan(const tq_paged_kv* kv, int B, int Hq, int64_t total_q, int max_q, int6
   const int rows = chunks ? kChunkRows : max_q * g;
   P.rows_per_item = rows <= 4 ? 4 : 8;                           // one or two column blocks
   P.row_blocks = (rows + P.rows_per_item - 1) / P.rows_per_item;
-  P.ctas = 2 * sm_count();
+  P.ctas = 2 * sm_count();                                       // as many as run at a time
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t items = (size_t)B * kv->Hkv * P.row_blocks, slots = items + P.ctas, pd = (size_t)kv->d * (kv->v_alg == 2 ? 2 : 1);
   size_t off = 0;
@@ -317,6 +317,7 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   if (((uintptr_t)q_start | (uintptr_t)kv_len | (uintptr_t)page_table | (uintptr_t)prefix_len | (uintptr_t)slopes) & 3)
     return fail(TQ_ERR_INVALID_ARG, f + ": int32 / fp32 arrays must be 4-byte aligned");
   if (!work) return TQ_OK;
+  if (window >= max_kv_len) window = 0;
   const int g = Hq / kv->Hkv;
   const Plan P = plan(kv, B, Hq, total_q, max_q_len, max_kv_len, prefix_len ? 0 : window);
   if (!ws || ws_bytes < tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len))

@@ -70,6 +70,21 @@ __device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, 
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same with zero for the sum so far
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
+__device__ __forceinline__ void mma_u8s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -196,7 +211,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
         const int jlo = row0 / p.g, jhi = min(rows - 1, row0 + RB - 1) / p.g;
         // ---- one part: blocks [pos, stop) of item (b, hkv, rb) ------------------------------------------------
         const int64_t stop = min(base + nb, start.end);
-        const int64_t t0 = lo + 16 * (pos - base), t1 = min(hi, lo + 16 * (stop - base));
+        const int t0 = (int)(lo + 16 * (pos - base)), t1 = (int)min(hi, lo + 16 * (stop - base));
         const int nblk = (int)(stop - pos);
         const int item = (b * p.Hkv + hkv) * p.row_blocks + rb;
         if (pos == base && threadIdx.x == 0) {
@@ -206,8 +221,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
         pos = stop;
 
         // this lane's query rows (c and c + 4 of the block)
-        int64_t qpos[NB];
-        float fac[NB], slope[NB], ref[NB], sum[NB], wsum[NB], zsum[NB], elim[NB];
+        int qpos[NB];
+        // ref is the reference (from: the same, 0 in the empty state), elim a power of two >= every value norm seen
+        // and room what its inverse times kRowRoom is
+        float fac[NB], slope[NB], ref[NB], from[NB], sum[NB], wsum[NB], zsum[NB], elim[NB], room[NB];
         int qsum[NB];
 #pragma unroll
         for (int u = 0; u < NB; ++u) {
@@ -215,13 +232,14 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           const bool on = row < rows;
           const int j = on ? row / p.g : 0, h = hkv * p.g + (on ? row - j * p.g : 0);
           const int64_t at = (int64_t)item * RB + c + 4 * u;
-          qpos[u] = on ? first + j : INT64_MIN / 2;
+          qpos[u] = on ? (int)first + j : -1;
           fac[u] = on ? p.key_fac * p.qs[at].x : 0.f;
           qsum[u] = on && KB == 4 ? __float_as_int(p.qs[at].y) : 0;
           slope[u] = on && p.slopes ? p.slopes[h] * kLog2e : 0.f;
           ref[u] = -INFINITY;
           sum[u] = wsum[u] = zsum[u] = 0.f;
-          elim[u] = 0.f;                                         // power of two >= every value norm seen
+          from[u] = elim[u] = 0.f;
+          room[u] = 1.f;
         }
         // query limbs: column 2 h + limb of block u is head row h + 4 u
         uint32_t qf[NB][D / 16];
@@ -236,13 +254,15 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
             qf[u][4 * i] = v.x, qf[u][4 * i + 1] = v.y, qf[u][4 * i + 2] = v.z, qf[u][4 * i + 3] = v.w;
           }
         }
-        float oc[MB][4], oz[ALG2 ? MB : 1][4];
+        // outputs: columns c and c + 4 of a product. With four rows the sign plane's go where the rows c + 4 would be
+        constexpr bool SHARE = ALG2 && NB == 1;
+        float oc[MB][4], oz[ALG2 && !SHARE ? MB : 1][4];
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             oc[m][i] = 0.f;
-            if (ALG2) oz[m][i] = 0.f;
+            if (ALG2 && !SHARE) oz[m][i] = 0.f;
           }
 
         // ---- the ring: where this lane's 16-byte chunks of a stage come from ----------------------------------
@@ -262,21 +282,24 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           unit[i] = 4 * len;
         }
         const int32_t* table = p.table + (int64_t)b * p.max_pages;
-        const int blk0 = (int)(t0 >> 4);                         // block number in the sequence
+        const int blk0 = t0 >> 4;                                // block number in the sequence
         auto page_of = [&](int blk) { return blk < nblk ? table[(blk0 + blk) >> (p.page_shift - 4)] : 0; };
         uint32_t absent = 0;                                     // stages whose page number is out of range
-        auto issue = [&](int blk, int page) {
+        auto issue = [&](int blk, int page, int s) {
           if (blk < nblk) {
-            const int s = (blk / kRowWarps) % kRowStages;
-            const bool good = page >= 0 && page < p.num_pages;
-            if (!good && lane == 0) atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
-            absent = good ? absent & ~(1u << s) : absent | (1u << s);
-            const int64_t u16 = good ? ((int64_t)page * p.Hkv + hkv) * units_per_page + ((blk0 + blk) & (units_per_page - 1)) : 0;
+            uint32_t bytes = 16;
+            if ((uint32_t)page >= (uint32_t)p.num_pages) {
+              if (lane == 0) atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+              absent |= 1u << s;
+              page = 0;
+              bytes = 0;
+            }
+            const uint32_t u16 = ((uint32_t)page * p.Hkv + hkv) * units_per_page + ((blk0 + blk) & (units_per_page - 1));
             const uint32_t dst = ring_u32 + (s * L::kWords + 4 * lane) * 4;
 #pragma unroll
             for (int i = 0; i < L::kIter; ++i)
               if (i + 1 < L::kIter || lane + 32 * i < L::kChunks)
-                cp_async16(dst + 512 * i, src[i] + u16 * unit[i], good ? 16u : 0u);
+                cp_async16(dst + 512 * i, src[i] + (uint64_t)u16 * unit[i], bytes);
           }
           cp_commit();
         };
@@ -285,28 +308,28 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
         for (int k = 0; k < kRowStages - 1; ++k) {
           const int page = page_next;
           page_next = page_of(warp + (k + 1) * kRowWarps);
-          issue(warp + k * kRowWarps, page);
+          issue(warp + k * kRowWarps, page, k);
         }
         // tokens [open_lo, open_hi) are seen by every row (and those before the prefix)
-        const int64_t open_lo = p.window > 0 ? first + jhi - p.window + 1 : 0, open_hi = min(first + jlo + 1, t1);
+        const int open_lo = p.window > 0 ? (int)first + jhi - p.window + 1 : 0, open_hi = min((int)first + jlo + 1, t1);
+        const int pre = (int)prefix, open_pre = min(pre, t1);
 
 #pragma unroll 1
-        for (int blk = warp; blk < nblk; blk += kRowWarps) {
+        for (int blk = warp, s = 0; blk < nblk; blk += kRowWarps, s = (s + 1) % kRowStages) {
           {
             const int page = page_next;
             page_next = page_of(blk + kRowStages * kRowWarps);
             cp_wait<kRowStages - 2>();
             __syncwarp();
             // the stage read in the previous turn is free: all lanes are past it
-            issue(blk + (kRowStages - 1) * kRowWarps, page);
+            issue(blk + (kRowStages - 1) * kRowWarps, page, (s + kRowStages - 1) % kRowStages);
           }
-          const int s = (blk / kRowWarps) % kRowStages;
           const uint32_t* st = ring + s * L::kWords;
           const uint32_t st_u32 = ring_u32 + s * (L::kWords * 4);
-          const int64_t t = t0 + 16 * blk;
+          const int t = t0 + 16 * blk;
 
           // ---- scores: high and low bytes of the levels against the query limbs ---------------------------------
-          int ah[NB][4] = {}, al[NB][4] = {};
+          int ah[NB][4], al[NB][4];
           {
             uint32_t wa[KB], wb[KB];
             const int grp = D == 128 ? c : c >> 1;
@@ -348,8 +371,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
                 const int ks = D == 128 ? s4 : s4 >> 1;
 #pragma unroll
                 for (int u = 0; u < NB; ++u) {
-                  mma_s8(ah[u], h[0], h[1], h[2], h[3], qf[u][2 * ks], qf[u][2 * ks + 1]);
-                  mma_u8s8(al[u], l[0], l[1], l[2], l[3], qf[u][2 * ks], qf[u][2 * ks + 1]);
+                  if (ks == 0) {
+                    mma_s8_first(ah[u], h[0], h[1], h[2], h[3], qf[u][0], qf[u][1]);
+                    mma_u8s8_first(al[u], l[0], l[1], l[2], l[3], qf[u][0], qf[u][1]);
+                  } else {
+                    mma_s8(ah[u], h[0], h[1], h[2], h[3], qf[u][2 * ks], qf[u][2 * ks + 1]);
+                    mma_u8s8(al[u], l[0], l[1], l[2], l[3], qf[u][2 * ks], qf[u][2 * ks + 1]);
+                  }
                 }
               }
             }
@@ -357,38 +385,45 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           // ---- softmax weights: tokens r, r + 8 of rows c, c + 4 ------------------------------------------------
           const uint16_t* kn = (const uint16_t*)(st + L::kKn);
           const uint16_t* vn = (const uint16_t*)(st + L::kVn);
-          float x[2][NB];                                        // [token][row]
-          const bool gone = (absent >> s) & 1;
-          const bool whole = !gone && ((t >= open_lo && t + 16 <= open_hi) || t + 16 <= min(prefix, t1));
-          float nk[2], nv[2];
+          float x[2][NB], n[2][NB], ga[2][NB];                   // [token][row]: score, value norm, residual norm
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int64_t tt = t + r + 8 * k;
-            const bool in = whole || (tt < t1 && !gone);         // within the range at all
-            nk[k] = in ? __half2float(__ushort_as_half(kn[r + 8 * k])) : 0.f;
-            nv[k] = in ? __half2float(__ushort_as_half(vn[r + 8 * k])) : 0.f;
+            const float nk = __half2float(__ushort_as_half(kn[r + 8 * k]));
+            const float nv = __half2float(__ushort_as_half(vn[r + 8 * k]));
+            const float ng = ALG2 ? __half2float(__ushort_as_half(((const uint16_t*)(st + L::kVg))[r + 8 * k])) : 0.f;
 #pragma unroll
             for (int u = 0; u < NB; ++u) {
-              const int sc = (ah[u][2 * k] << 8) + ah[u][2 * k + 1] + al[u][2 * k] + ((al[u][2 * k + 1] + qsum[u]) >> 8);
-              float v = (float)sc * (nk[k] * fac[u]);
+              int sc = (ah[u][2 * k] << 8) + ah[u][2 * k + 1] + al[u][2 * k];
+              sc += KB == 4 ? (al[u][2 * k + 1] + qsum[u]) >> 8 : al[u][2 * k + 1] >> 8;
+              float v = (float)sc * (nk * fac[u]);
               if (p.cap_log2 > 0.f) v = capped(v * p.cap2x, p.cap_log2);
-              if (p.slopes) v += slope[u] * (float)(tt - qpos[u]);
-              if (!whole) {
-                const bool see = in && qpos[u] > INT64_MIN / 4 &&
-                                 ((tt <= qpos[u] && (p.window == 0 || tt > qpos[u] - p.window)) || tt < prefix);
-                v = see ? v : -INFINITY;
-              }
+              if (p.slopes) v = fmaf(slope[u], (float)(t + r + 8 * k - qpos[u]), v);
               x[k][u] = v;
+              n[k][u] = nv;
+              ga[k][u] = ng;
             }
           }
-          // largest score and largest finite value norm that a row sees
+          if (absent != 0 || !((t >= open_lo && t + 16 <= open_hi) || t + 16 <= open_pre)) {
+            const bool gone = (absent >> s) & 1;
+            absent &= ~(1u << s);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int tt = t + r + 8 * k;
+#pragma unroll
+              for (int u = 0; u < NB; ++u)
+                if (gone || tt >= t1 || !((tt <= qpos[u] && (p.window == 0 || tt > qpos[u] - p.window)) || tt < pre)) {
+                  x[k][u] = -INFINITY;                           // not seen; its norms may be anything
+                  n[k][u] = ga[k][u] = 0.f;
+                }
+            }
+          }
+          // largest score and largest value norm that a row sees (a norm that is not finite has no say)
           float top[NB], topn[NB];
           bool move = false;
 #pragma unroll
           for (int u = 0; u < NB; ++u) {
             top[u] = fmaxf(x[0][u], x[1][u]);
-            topn[u] = fmaxf(x[0][u] > -INFINITY && nv[0] < INFINITY ? nv[0] : 0.f,
-                            x[1][u] > -INFINITY && nv[1] < INFINITY ? nv[1] : 0.f);
+            topn[u] = fmaxf(n[0][u], n[1][u]);
             move |= top[u] > ref[u] + kRowLazy || topn[u] > elim[u];
           }
           if (__any_sync(0xffffffffu, move)) {
@@ -407,11 +442,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
               ref[u] = nr;
               sum[u] *= fs;
               f[u] = fs;
+              from[u] = nr == -INFINITY ? 0.f : nr;
               if (topn[u] > elim[u]) {
                 // the norm limit: the next power of two (the exponent field of the largest norm, plus one)
-                const float el = __int_as_float((__float_as_int(topn[u]) & 0x7F800000) + 0x00800000);
+                const float el = __int_as_float((__float_as_int(fminf(topn[u], 65504.f)) & 0x7F800000) + 0x00800000);
                 f[u] *= elim[u] / el;
                 elim[u] = el;
+                room[u] = kRowRoom / el;
               }
               wsum[u] *= f[u];
               zsum[u] *= f[u];
@@ -420,9 +457,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
             for (int q = 0; q < MB; ++q)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if ((i & 1) < NB) {
+                if ((i & 1) < NB || SHARE) {
                   oc[q][i] *= f[i & 1 & (NB - 1)];
-                  if (ALG2) oz[q][i] *= f[i & 1 & (NB - 1)];
+                  if (ALG2 && !SHARE) oz[q][i] *= f[i & 1 & (NB - 1)];
                 }
           }
           uint32_t pc[2], pz[2];
@@ -431,22 +468,19 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
             float w[2] = {0.f, 0.f};
 #pragma unroll
             for (int u = 0; u < NB; ++u) {
-              const float e = ex2_approx(x[k][u] - (ref[u] == -INFINITY ? 0.f : ref[u]));
+              const float e = ex2_approx(x[k][u] - from[u]);
               sum[u] += e;
-              const float n = elim[u] > 0.f ? nv[k] * (kRowRoom / elim[u]) : nv[k];
-              w[u] = x[k][u] == -INFINITY ? 0.f : e * n;         // an unseen token's norm may be anything
+              w[u] = e * (n[k][u] * room[u]);
               if (VB == 1) wsum[u] += w[u];
             }
             pc[k] = transpose8x8(half2_of(w[0], w[1]));
             if constexpr (ALG2) {
-              const uint16_t* vg = (const uint16_t*)(st + L::kVg);
-              const float ga = __half2float(__ushort_as_half(vg[r + 8 * k]));
 #pragma unroll
               for (int u = 0; u < NB; ++u) {
-                w[u] = x[k][u] == -INFINITY ? 0.f : w[u] * ga;
+                w[u] *= ga[k][u];
                 zsum[u] += w[u];
               }
-              pz[k] = transpose8x8(half2_of(w[0], w[1]));
+              pz[k] = transpose8x8(SHARE ? half2_of(0.f, w[0]) : half2_of(w[0], w[1]));
             }
           }
           // ---- values ----------------------------------------------------------------------------------
@@ -495,7 +529,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
                         __byte_perm(e[2][h], e[3][h], 0x5410u), __byte_perm(e[2][h], e[3][h], 0x7632u), pc[0], pc[1]);
             }
           }
-          if constexpr (ALG2) plane(L::kSign, oz, pz[0], pz[1]);
+          if constexpr (SHARE) plane(L::kSign, oc, pz[0], pz[1]);
+          else if constexpr (ALG2) plane(L::kSign, oz, pz[0], pz[1]);
         }
 
         // ---- merge the warps' states --------------------------------------------------------------------------
@@ -520,13 +555,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           auto inv_bit = [](int i) {
             return i < 10 ? __int_as_float((127 + 24 - i) << 23) : __int_as_float((127 + 15 - (1 << (i - 10))) << 23);
           };
-          auto put = [&](float (&o)[MB][4], int at, bool one_bit, float total, float unit) {
+          auto put = [&](float (&o)[MB][4], int odd, int at, bool one_bit, float total, float unit) {
             unit *= elim[u];
 #pragma unroll
             for (int m = 0; m < MB; ++m)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float v = o[m][2 * h + u];
+                const float v = o[m][2 * h + odd];
                 if (one_bit) {
                   const int i = D == 128 ? m + 8 * h : r + 8 * h;
                   dst[at + (D == 128 ? 16 * r : 16 * m) + i] = (i == 15 ? -v : fmaf(2.f * v, inv_bit(i), -total)) * unit;
@@ -535,8 +570,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
                 }
               }
           };
-          put(oc, 0, VB == 1, wsum[u], p.v_inv_unit / kRowRoom);
-          if constexpr (ALG2) put(oz, D, true, zsum[u], 1.f / kRowRoom);
+          put(oc, u, 0, VB == 1, wsum[u], p.v_inv_unit / kRowRoom);
+          if constexpr (SHARE) put(oc, 1, D, true, zsum[u], 1.f / kRowRoom);
+          else if constexpr (ALG2) put(oz, u, D, true, zsum[u], 1.f / kRowRoom);
         }
         __syncthreads();
         const int live = min(RB, rows - row0);
@@ -546,12 +582,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           float best = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kRowWarps; ++w) best = fmaxf(best, mg[(w * RB + row) * RS + PD]);
-          const float from = best == -INFINITY ? 0.f : best;
+          const float base_ref = best == -INFINITY ? 0.f : best;
           float o = 0.f, l = 0.f;
 #pragma unroll
           for (int w = 0; w < kRowWarps; ++w) {
             const float* m = mg + (w * RB + row) * RS;
-            const float f = ex2_approx(m[PD] - from);
+            const float f = ex2_approx(m[PD] - base_ref);
             o += f * m[i];
             l += f * m[PD + 1];
           }
