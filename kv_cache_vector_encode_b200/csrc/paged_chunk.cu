@@ -382,9 +382,10 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
 }
 
 // ---- chunk ----------------------------------------------------------------------------------------------
-// Warps 0-3 and 4-7: the softmax of query rows 0-127 and 128-255 (thread = row); warp 8 copies tiles; warp 9 owns
-// TMEM and issues the products. TMEM: scores S0, S1 (128 columns each; the weights P take the place of the
-// first 64 as fp16 pairs), outputs O0, O1 (D columns each).
+// Warps 0-3 and 4-7: the softmax of query rows 0-127 and 128-255, thread = row (two threads to a row, which hide more
+// latency but have to exchange their maxima, take 1.25 times as long); warp 8 copies tiles; warp 9 owns TMEM and
+// issues the products. TMEM: scores S0, S1 (128 columns each; the weights P take the place of the first 64 as fp16
+// pairs), outputs O0, O1 (D columns each).
 // The products run in the order S0 S1 | PV0 S0' | PV1 S1' | ..., so that one group's softmax overlaps the other
 // group's products. They complete in order: when a group's next scores are there, its PV product before them is
 // done, and the group may rescale its output in TMEM before it hands over the next weights.
@@ -397,15 +398,15 @@ struct ChunkLayout {
 constexpr int kChunkThreads = 320;
 constexpr int kChunkCols = 512;
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
       "%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -428,10 +429,43 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 
 enum CBars { Q_FULL = 0, KV_FULL = 2, KV_EMPTY = 10, S_FULL = 18, P_FULL = 20, O_FULL = 22, CNBARS = 24 };
 
-// bits [0, n) of the 32 columns from c0 on, where n counts from column 0 of the tile
-__device__ __forceinline__ uint32_t below(int64_t n, int c0) {
-  const int64_t k = n - c0;
-  return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+// the n lowest bits of 32
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
+// tanh(u) = u + u^3 (c0 + c1 u^2 + c2 u^4) for |u| <= 0.6, fitted to the least largest error of tanh there (9e-7).
+constexpr float kTanhReach = 0.6f, kTanh0 = -0.33314597f, kTanh1 = 0.13050765f, kTanh2 = -0.04072624f;
+
+// Scores of a row's consecutive tokens, the first of them `ahead` of the query, into the log2 domain: times f, capped,
+// biased. A cap costs two more special-function results per score than the softmax's one; where no score of
+// the warp passes 0.6 of it (almost everywhere), the polynomial takes their place.
+template <int N>
+__device__ __forceinline__ void shape(const PagedAttendParams& p, float (&s)[N], float f, float slope, int ahead) {
+  if (p.cap_log2 > 0.f) {
+    const float fu = f * (0.5f * p.cap2x * 0.69314718f);         // u = score / cap, both in one domain
+    float m4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(s[i]));
+    const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    if (__all_sync(0xffffffffu, most * fu <= kTanhReach)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float u = s[i] * fu, w = u * u;
+        const float q = fmaf(fmaf(kTanh2, w, kTanh1), w, kTanh0);
+        s[i] = p.cap_log2 * fmaf(q * w, u, u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = capped(s[i] * f * p.cap2x, p.cap_log2);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] *= f;
+  }
+  if (p.slopes) {
+    const float near = slope * (float)ahead;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += fmaf(slope, (float)i, near);
+  }
 }
 
 template <int D>
@@ -549,13 +583,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (ok && j + 1 < n) free_stage(kn);
     }
   } else if (warp < 4 || two) {
-    const int u = warp >> 2, r = tid & 127;
+    const int u = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lane_base + 128 * u, to = tbase + lane_base + 256 + D * u;
     const int row = row0 + 128 * u + r;
     const bool on = row < rows;
     const int jq = on ? row / p.g : 0, h = x.hkv * p.g + (on ? row - jq * p.g : 0);
-    const int64_t pos = x.first + jq;
+    const int pos = (int)x.first + jq;
     // ---- this row's query: fp16 times a power of two (exact for what lies within 2^-26 of its largest) -----
     float fac;
     {
@@ -588,50 +622,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (lane == 0) mbar_arrive(&bar[Q_FULL + u]);
     }
     const float slope = p.slopes ? p.slopes[h] * kLog2e : 0.f;
+    const bool shaped = p.cap_log2 > 0.f || p.slopes != nullptr;
     float ref = -INFINITY, sum = 0.f;
     // the group's first and last position, for tiles that every row sees whole
-    const int64_t pmin = x.first + (row0 + 128 * u) / p.g, pmax = x.first + (min(rows, row0 + 128 * u + 128) - 1) / p.g;
+    const int pmin = (int)x.first + (row0 + 128 * u) / p.g, pmax = (int)x.first + (min(rows, row0 + 128 * u + 128) - 1) / p.g;
+    const int pre = (int)x.prefix;
     const TileHead* heads = c.heads + item0;
-    int64_t t0 = unit_t0 + (int64_t)tile0 * kTile;
+    int t0 = (int)unit_t0 + tile0 * kTile;
     bool ok = true;
+#pragma unroll 1
     for (int j = 0; j < n; ++j, t0 += kTile) {
       const float4 hd = *(const float4*)&heads[j];
       const uint32_t flags = __float_as_uint(hd.w);
       ok = mbar_wait_warp(&bar[S_FULL + u], j & 1, p.err, kDevTimeoutMma, abort_flag);
       if (!ok) break;
-      tc_fence_after();
+     tc_fence_after();
       float s[kTile];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
       tmem_ld_wait();
       float f = fac * hd.x;
-      const bool whole = flags == 0 && ((t0 + kTile - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window)) || t0 + kTile <= x.prefix);
-      if (p.cap_log2 > 0.f || p.slopes || !whole) {
-        const float near = slope * (float)(t0 - pos);
-#pragma unroll
-        for (int i = 0; i < kTile; ++i) s[i] *= f;
-        if (p.cap_log2 > 0.f) {
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] = capped(s[i] * p.cap2x, p.cap_log2);
-        }
-        if (p.slopes) {
-#pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] += fmaf(slope, (float)i, near);
-        }
+      const bool whole = flags == 0 && ((t0 + kTile - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window)) || t0 + kTile <= pre);
+      if (shaped || !whole) {
+        shape(p, s, f, slope, t0 - pos);
         f = 1.f;
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // seen: present and ((t <= pos and t > pos - window) or t < prefix)
-            uint32_t m = below(pos + 1 - t0, 32 * i);
-            if (p.window > 0) m &= ~below(pos - p.window + 1 - t0, 32 * i);
-            m |= below(x.prefix - t0, 32 * i);
+            const int at = t0 + 32 * i;
+            uint32_t m = below(pos + 1 - at);
+            if (p.window > 0) m &= ~below(pos - p.window + 1 - at);
+            m |= below(pre - at);
             m = on ? m & __ldg(&heads[j].present[i]) : 0u;
             const uint32_t strange = flags & 2u ? m & __ldg(&heads[j].strange[i]) : 0u;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              s[32 * i + k] = (m >> k) & 1 ? s[32 * i + k] : -INFINITY;
-              if (flags & 2u) s[32 * i + k] = (strange >> k) & 1 ? __int_as_float(0x7FC00000) : s[32 * i + k];
+            for (int k = 0; k < 32; ++k) s[32 * i + k] = (m >> k) & 1 ? s[32 * i + k] : -INFINITY;
+            if (strange) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[32 * i + k] = (strange >> k) & 1 ? __int_as_float(0x7FC00000) : s[32 * i + k];
             }
           }
         }
@@ -657,7 +686,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
       }
-      const float off = hd.y - (ref == -INFINITY ? 0.f : ref);
+     const float off = hd.y - (ref == -INFINITY ? 0.f : ref);
       float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < kTile; i += 32) {
@@ -672,7 +701,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         tmem_st16(ts + i / 2, w);
       }
-      tmem_st_wait();
+     tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[P_FULL + u]);
