@@ -34,8 +34,11 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 128;            // tokens of a tile
+constexpr int kHalf = kTile / 2;      // tokens of a step of the attention
 constexpr int kCtaRows = 256;         // query rows of a CTA: two groups of 128
-constexpr float kLazy = 8.0f;         // how far (log2) a score may pass the reference before it moves
+// How far (log2) a score may pass the reference before it moves: weights then stay below 2^14, within fp16. What is 2^14
+// below the largest weight of a row no longer counts to a precision of 2^-25 of it.
+constexpr float kLazy = 14.0f;
 constexpr int kBits = 12;             // operands: norms below 1 after the tile's exponent, times 2^kBits
 
 // What the attention needs to know of a tile besides its operands.
@@ -382,20 +385,21 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
 }
 
 // ---- chunk ----------------------------------------------------------------------------------------------
-// Warps 0-3 and 4-7: the softmax of query rows 0-127 and 128-255, thread = row (two threads to a row, which hide more
-// latency but have to exchange their maxima, take 1.25 times as long); warp 8 copies tiles; warp 9 owns TMEM and
-// issues the products. TMEM: scores S0, S1 (128 columns each; the weights P take the place of the first 64 as fp16
-// pairs), outputs O0, O1 (D columns each).
-// The products run in the order S0 S1 | PV0 S0' | PV1 S1' | ..., so that one group's softmax overlaps the other
-// group's products. They complete in order: when a group's next scores are there, its PV product before them is
-// done, and the group may rescale its output in TMEM before it hands over the next weights.
+// Warps 0-3 and 4-7: the softmax of query rows 0-127 and 128-255, thread = row; warp 8 copies tiles; warps 9 and 10
+// issue the products, one for each group; warp 9 owns TMEM. TMEM per group: scores of two half tiles (64 columns each;
+// the weights P take the place of the first 32 as fp16 pairs), output O (D columns).
+// A group's step i is a half tile of 64 tokens: scores S(i), softmax, O += P(i) V(i). S(i + 2) follows PV(i) into the
+// same columns, so that the next step's scores are there when a softmax ends, and the softmax warps never wait for
+// a product that waits for them. (Whole tiles leave TMEM for one score buffer per group: the chain softmax, PV, next
+// scores, softmax then takes 4200 cycles per 256 x 128 scores, of which the tensor cores work 2048. Half tiles
+// take 3700: a 128 x 64 score product takes as long as a 128 x 128 one, its queries' way out of shared memory.)
 template <int D>
 struct ChunkLayout {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kImg = 128 * D * 2, kQ = 0, kRing = 2 * kImg, kBar = kRing + kStages * kImg,
                             kTotal = kBar + 256 + 1024;
 };
-constexpr int kChunkThreads = 320;
+constexpr int kChunkThreads = 352;
 constexpr int kChunkCols = 512;
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
@@ -416,56 +420,142 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 pairs of A's K in a column.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// Products with descriptors in two words, of which only the low one (the address) changes: K-major operands with the
+// 128-byte swizzle, as desc_kmajor_sw128 makes them.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr) { return (smem_addr >> 4) | (1u << 16); }
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+      : "memory");
+}
+// A in TMEM: fp16 pairs of its K in a column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
 
-enum CBars { Q_FULL = 0, KV_FULL = 2, KV_EMPTY = 10, S_FULL = 18, P_FULL = 20, O_FULL = 22, CNBARS = 24 };
+// A wait that is expected to be short: polls before it settles down to the bounded wait.
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t phase, uint32_t* err, uint32_t code, volatile uint32_t* abort) {
+  bool ok = false;
+#pragma unroll 1
+  for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, phase);
+  return __all_sync(0xffffffffu, ok || mbar_wait_slow(bar, phase, err, code, abort));
+}
+
+// S_FULL, P_FULL: [group][half]
+enum CBars { Q_FULL = 0, KV_FULL = 2, KV_EMPTY = 10, S_FULL = 18, P_FULL = 22, PV_DONE = 26, CNBARS = 28 };
 
 // the n lowest bits of 32
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-// tanh(u) = u + u^3 (c0 + c1 u^2 + c2 u^4) for |u| <= 0.6, fitted to the least largest error of tanh there (9e-7).
-constexpr float kTanhReach = 0.6f, kTanh0 = -0.33314597f, kTanh1 = 0.13050765f, kTanh2 = -0.04072624f;
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Scores of a row's consecutive tokens, the first of them `ahead` of the query, into the log2 domain: times f, capped,
-// biased. A cap costs two more special-function results per score than the softmax's one; where no score of
-// the warp passes 0.6 of it (almost everywhere), the polynomial takes their place.
+// 2^x of two numbers below 2^7 without the special-function unit, which bounds the softmax (8 cycles per warp and
+// exponential): x = i + r by rounding, 2^r on [-1/2, 1/2] by a cubic fitted to the least largest relative error (7.5e-5,
+// a third of an fp16 rounding), i into the exponent. Below 2^-126 the result is 2^-126.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 t = add2(x, both(12582912.f));                    // 1.5 2^23: the integer in the low bits
+  const float2 r = add2(x, mul2(add2(t, both(-12582912.f)), both(-1.f)));
+  float2 y = fma2(both(0.05517167f), r, both(0.24261113f));
+  y = fma2(y, r, both(0.69326099f));
+  y = fma2(y, r, both(0.99992807f));
+  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+}
+
+// Which of 16 pairs take the polynomial: three of eight balance the two units.
+__device__ __forceinline__ constexpr bool by_poly(int k) { return (k & 7) == 1 || (k & 7) == 4 || (k & 7) == 6; }
+
+// tanh(u) = u + u^3 q(u^2) with q of degree 2 for |u| <= 0.6 (largest error of tanh 9e-7) and of degree 4 for
+// |u| <= 1 (3.2e-7), fitted to the least largest error.
+template <int N, int DEG>
+__device__ __forceinline__ void tanh_poly(float (&s)[N], float fu) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 u = mul2(make_float2(s[i], s[i + 1]), both(fu)), w = mul2(u, u);
+    float2 q;
+    if (DEG == 2) {
+      q = fma2(both(-0.04072624f), w, both(0.13050765f));
+      q = fma2(q, w, both(-0.33314597f));
+    } else {
+      q = fma2(both(-0.00298308f), w, both(0.01653281f));
+      q = fma2(q, w, both(-0.05142535f));
+      q = fma2(q, w, both(0.13275615f));
+      q = fma2(q, w, both(-0.33328670f));
+    }
+    const float2 x = fma2(mul2(q, w), u, u);
+    s[i] = x.x, s[i + 1] = x.y;
+  }
+}
+
+// Scores of a row's consecutive tokens, the first of them `ahead` of the query: what they times the factor returned are
+// in the log2 domain, capped and biased. A cap costs two more special-function results per score than the
+// softmax's one; where no score of the warp reaches the cap, a polynomial takes their place.
 template <int N>
-__device__ __forceinline__ void shape(const PagedAttendParams& p, float (&s)[N], float f, float slope, int ahead) {
+__device__ __forceinline__ float shape(const PagedAttendParams& p, float (&s)[N], float f, float slope, int ahead) {
   if (p.cap_log2 > 0.f) {
     const float fu = f * (0.5f * p.cap2x * 0.69314718f);         // u = score / cap, both in one domain
     float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(s[i]));
-    const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-    if (__all_sync(0xffffffffu, most * fu <= kTanhReach)) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float u = s[i] * fu, w = u * u;
-        const float q = fmaf(fmaf(kTanh2, w, kTanh1), w, kTanh0);
-        s[i] = p.cap_log2 * fmaf(q * w, u, u);
-      }
+    const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * fu;
+    if (__all_sync(0xffffffffu, most <= 0.6f)) {
+      tanh_poly<N, 2>(s, fu);
+    } else if (__all_sync(0xffffffffu, most <= 1.f)) {
+      tanh_poly<N, 4>(s, fu);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[i] = capped(s[i] * f * p.cap2x, p.cap_log2);
+      for (int i = 0; i < N; ++i) s[i] = capped(s[i] * f * p.cap2x, 1.f);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] *= f;
+    f = p.cap_log2;
   }
   if (p.slopes) {
     const float near = slope * (float)ahead;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += fmaf(slope, (float)i, near);
+    for (int i = 0; i < N; ++i) s[i] = fmaf(s[i], f, fmaf(slope, (float)i, near));
+    f = 1.f;
   }
+  return f;
 }
 
 template <int D>
@@ -494,13 +584,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (tid == 0) {
     for (int u = 0; u < 2; ++u) {
       mbar_init(&bar[Q_FULL + u], 4);
-      mbar_init(&bar[S_FULL + u], 1);
-      mbar_init(&bar[P_FULL + u], 4);
-      mbar_init(&bar[O_FULL + u], 1);
+      mbar_init(&bar[PV_DONE + u], 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&bar[S_FULL + 2 * u + k], 1);
+        mbar_init(&bar[P_FULL + 2 * u + k], 4);
+      }
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bar[KV_FULL + s], 1);
-      mbar_init(&bar[KV_EMPTY + s], 1);
+      mbar_init(&bar[KV_EMPTY + s], two ? 2 : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -527,60 +619,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int i = max(0, k - NS); i < k; ++i) mbar_wait(&bar[KV_FULL + i % NS], (i / NS) & 1, nullptr, 0, nullptr);
     }
     __syncwarp();
-  } else if (warp == 9) {
-    const uint32_t ring = smem_u32(smem + L::kRing), q = smem_u32(smem + L::kQ);
-    const int groups = two ? 2 : 1;
-    auto scores = [&](int u, int k) {
-      if (elect_one_sync()) {
-        const uint32_t b = ring + (k % NS) * L::kImg;
+  } else if (warp >= 9) {
+    // ---- products of group u ---------------------------------------------------------------------------------
+    const int u = warp - 9;
+    const uint32_t ring = desc_low(smem_u32(smem + L::kRing)), q = desc_low(smem_u32(smem + L::kQ) + u * L::kImg);
+    const uint32_t ts = tbase + 128 * u, to = tbase + 256 + D * u;
+    const bool leader = elect_one_sync();
+    auto wait = [&](int b, int ph, uint32_t code) { return wait_soon(&bar[b], ph & 1, p.err, code, abort_flag); };
+    // scores of half tile i; the second half is the last use of the keys' stage
+    auto scores = [&](int i) {
+      const int half = i & 1, stage = (i & ~1) % NS;
+      const uint32_t b = ring + stage * (L::kImg >> 4) + half * (8192 >> 4);
+      if (leader) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
-          mma_f16_ss(tbase + 128 * u, desc_kmajor_sw128(q + u * L::kImg + at), desc_kmajor_sw128(b + at),
-                     idesc_f16_f32(128, 128), ks > 0);
+          const uint32_t at = ((ks >> 2) * 16384u + (ks & 3) * 32u) >> 4;
+          mma_ss(ts + 64 * half, q + at, b + at, idesc_f16_f32(128, 64), ks > 0);
         }
-        mma_commit(&bar[S_FULL + u]);
+        mma_commit(&bar[S_FULL + 2 * u + half]);
+        if (half) mma_commit(&bar[KV_EMPTY + stage]);
       }
       __syncwarp();
     };
-    auto free_stage = [&](int k) {
-      if (elect_one_sync()) mma_commit(&bar[KV_EMPTY + k % NS]);
-      __syncwarp();
-    };
-    auto wait = [&](int b, int ph, uint32_t code) {
-      const bool ok = mbar_wait_warp(&bar[b], ph & 1, p.err, code, abort_flag);
+    if (n > 0 && (u == 0 || two)) {
+      bool ok = wait(KV_FULL, 0, kDevTimeoutLoad) && wait(Q_FULL + u, 0, kDevTimeoutSync);
       tc_fence_after();
-      return ok;
-    };
-    bool ok = n > 0 && wait(KV_FULL, 0, kDevTimeoutLoad);
-    for (int u = 0; ok && u < groups; ++u) {
-      ok = wait(Q_FULL + u, 0, kDevTimeoutSync);
-      if (ok) scores(u, 0);
-    }
-    if (ok) free_stage(0);
-    for (int j = 0; ok && j < n; ++j) {
-      const int kv = 2 * j + 1, kn = 2 * j + 2;                  // this tile's V, the next one's K
-      ok = wait(KV_FULL + kv % NS, kv / NS, kDevTimeoutLoad);
-      for (int u = 0; ok && u < groups; ++u) {
-        ok = wait(P_FULL + u, j, kDevTimeoutSync);
+      if (ok) {
+        scores(0);
+        scores(1);
+      }
+#pragma unroll 1
+      for (int i = 0; ok && i < 2 * n; ++i) {
+        const int half = i & 1, kv = i | 1, kn = (i & ~1) + 2;   // stages: this tile's V, the next one's K
+        const bool more = i + 2 < 2 * n;
+        if (!half) ok = wait(KV_FULL + kv % NS, kv / NS, kDevTimeoutLoad) && (!more || wait(KV_FULL + kn % NS, kn / NS, kDevTimeoutLoad));
+        ok = ok && wait(P_FULL + 2 * u + half, i >> 1, kDevTimeoutSync);
         if (!ok) break;
-        if (elect_one_sync()) {
-          const uint32_t b = ring + (kv % NS) * L::kImg;
+        tc_fence_after();
+        const uint32_t b = ring + (kv % NS) * (L::kImg >> 4) + half * (D * 8);
+        if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_f16_ts(tbase + 256 + D * u, tbase + 128 * u + 8 * ks,
-                       desc_kmajor_sw128(b + (ks >> 2) * (D * 128u) + (ks & 3) * 32u), idesc_f16_f32(128, D),
-                       j > 0 || ks > 0);
-          if (j + 1 == n) mma_commit(&bar[O_FULL + u]);
+          for (int ks = 0; ks < kTile / 32; ++ks)
+            mma_ts(to, ts + 64 * half + 8 * ks, b + 2 * ks, idesc_f16_f32(128, D), i > 0 || ks > 0);
+          mma_commit(&bar[PV_DONE + u]);
+          if (half) mma_commit(&bar[KV_EMPTY + kv % NS]);
         }
         __syncwarp();
-        if (j + 1 < n) {
-          if (u == 0) ok = wait(KV_FULL + kn % NS, kn / NS, kDevTimeoutLoad);
-          if (ok) scores(u, kn);
-        }
+        if (more) scores(i + 2);
       }
-      if (ok) free_stage(kv);
-      if (ok && j + 1 < n) free_stage(kn);
     }
   } else if (warp < 4 || two) {
     const int u = warp >> 2, r = (warp & 3) * 32 + lane;
@@ -628,87 +714,94 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int pmin = (int)x.first + (row0 + 128 * u) / p.g, pmax = (int)x.first + (min(rows, row0 + 128 * u + 128) - 1) / p.g;
     const int pre = (int)x.prefix;
     const TileHead* heads = c.heads + item0;
-    int t0 = (int)unit_t0 + tile0 * kTile;
+    int t0 = (int)unit_t0 + tile0 * kTile;                       // first token of the half tile
     bool ok = true;
+    float4 hd = n > 0 ? *(const float4*)&heads[0] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int j = 0; j < n; ++j, t0 += kTile) {
-      const float4 hd = *(const float4*)&heads[j];
-      const uint32_t flags = __float_as_uint(hd.w);
-      ok = mbar_wait_warp(&bar[S_FULL + u], j & 1, p.err, kDevTimeoutMma, abort_flag);
+    for (int i = 0; i < 2 * n; ++i, t0 += kHalf) {
+      const int half = i & 1;
+      const TileHead* head = heads + (i >> 1);
+      const float4 cur = hd;
+      if (half && i + 1 < 2 * n) hd = *(const float4*)(head + 1);
+      const uint32_t flags = __float_as_uint(cur.w);
+      ok = wait_soon(&bar[S_FULL + 2 * u + half], (i >> 1) & 1, p.err, kDevTimeoutMma, abort_flag);
       if (!ok) break;
-     tc_fence_after();
-      float s[kTile];
+      tc_fence_after();
+      float s[kHalf];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+      for (int k = 0; k < kHalf; k += 32) tmem_ld32(ts + 64 * half + k, s + k);
       tmem_ld_wait();
-      float f = fac * hd.x;
-      const bool whole = flags == 0 && ((t0 + kTile - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window)) || t0 + kTile <= pre);
-      if (shaped || !whole) {
-        shape(p, s, f, slope, t0 - pos);
-        f = 1.f;
-        if (!whole) {
+      float f = fmaxf(fac * cur.x, 1.2e-38f);                    // not zero: it meets infinite scores
+      const bool whole = flags == 0 && ((t0 + kHalf - 1 <= pmin && (p.window == 0 || t0 > pmax - p.window)) || t0 + kHalf <= pre);
+      if (shaped) f = shape(p, s, f, slope, t0 - pos);
+      if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // seen: present and ((t <= pos and t > pos - window) or t < prefix)
-            const int at = t0 + 32 * i;
-            uint32_t m = below(pos + 1 - at);
-            if (p.window > 0) m &= ~below(pos - p.window + 1 - at);
-            m |= below(pre - at);
-            m = on ? m & __ldg(&heads[j].present[i]) : 0u;
-            const uint32_t strange = flags & 2u ? m & __ldg(&heads[j].strange[i]) : 0u;
+        for (int w = 0; w < kHalf / 32; ++w) {
+          // seen: present and ((t <= pos and t > pos - window) or t < prefix)
+          const int at = t0 + 32 * w;
+          uint32_t m = below(pos + 1 - at);
+          if (p.window > 0) m &= ~below(pos - p.window + 1 - at);
+          m |= below(pre - at);
+          m = on ? m & __ldg(&head->present[2 * half + w]) : 0u;
+          if ((flags & 2u) && (m & __ldg(&head->strange[2 * half + w]))) sum = __int_as_float(0x7FC00000);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[32 * i + k] = (m >> k) & 1 ? s[32 * i + k] : -INFINITY;
-            if (strange) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) s[32 * i + k] = (strange >> k) & 1 ? __int_as_float(0x7FC00000) : s[32 * i + k];
-            }
-          }
+          for (int k = 0; k < 32; ++k) s[32 * w + k] = (m >> k) & 1 ? s[32 * w + k] : -INFINITY;
         }
       }
-      float m4[4] = {s[0], s[1], s[2], s[3]};
+      float m8[8];
 #pragma unroll
-      for (int i = 4; i < kTile; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
-      const float top = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f, hd.y);
+      for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[k + 8]);
+#pragma unroll
+      for (int t = 16; t < kHalf; t += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = fmaxf(fmaxf(m8[k], s[t + k]), s[t + k + 8]);
+      const float top = fmaf(fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))),
+                             f, cur.y);
       if (__any_sync(0xffffffffu, top > ref + kLazy)) {
         const float nr = fmaxf(ref, top);
         const float g = nr == ref ? 1.f : ex2_approx(ref - nr);  // 0 from the empty state
         ref = nr;
         sum *= g;
-        if (j > 0) {
+        if (i > 0) {
+          ok = wait_soon(&bar[PV_DONE + u], (i - 1) & 1, p.err, kDevTimeoutMma, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < D; i += 16) {
-            uint32_t o[16];
-            tmem_ld16(to + i, o);
+          for (int k = 0; k < D; k += 32) {
+            float o[32];
+            tmem_ld32(to + k, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
-            tmem_st16(to + i, o);
+            for (int e = 0; e < 32; ++e) o[e] *= g;
+            tmem_st16(to + k, reinterpret_cast<const uint32_t*>(o));
+            tmem_st16(to + k + 16, reinterpret_cast<const uint32_t*>(o) + 16);
           }
         }
       }
-     const float off = hd.y - (ref == -INFINITY ? 0.f : ref);
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      // weights, in fp16 into the place of the scores
+      const float2 off = both(cur.y - (ref == -INFINITY ? 0.f : ref)), f2 = both(f);
+      float2 l2[2] = {both(0.f), both(0.f)};
 #pragma unroll
-      for (int i = 0; i < kTile; i += 32) {
+      for (int t = 0; t < kHalf; t += 32) {
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const float a = ex2_approx(fmaf(s[i + 2 * k], f, off)), b = ex2_approx(fmaf(s[i + 2 * k + 1], f, off));
-          l4[(2 * k) & 3] += a;
-          l4[(2 * k + 1) & 3] += b;
-          const __half2 h2 = __floats2half2_rn(a, b);
+          const float2 x = fma2(make_float2(s[t + 2 * k], s[t + 2 * k + 1]), f2, off);
+          const float2 e = by_poly(k) ? exp2_poly(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          l2[k & 1] = add2(l2[k & 1], e);
+          const __half2 h2 = __floats2half2_rn(e.x, e.y);
           w[k] = *reinterpret_cast<const uint32_t*>(&h2);
         }
-        tmem_st16(ts + i / 2, w);
+        tmem_st16(ts + 64 * half + t / 2, w);
       }
-     tmem_st_wait();
+      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[P_FULL + u]);
-      sum = fmaf((l4[0] + l4[1]) + (l4[2] + l4[3]), hd.z, sum);
+      if (lane == 0) mbar_arrive(&bar[P_FULL + 2 * u + half]);
+      sum = fmaf((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y), cur.z, sum);
     }
     // ---- out = O / sum ------------------------------------------------------------------------------------
-    if (n > 0 && ok) ok = mbar_wait_warp(&bar[O_FULL + u], 0, p.err, kDevTimeoutMma, abort_flag);
+    if (n > 0 && ok) ok = wait_soon(&bar[PV_DONE + u], 1, p.err, kDevTimeoutMma, abort_flag);   // of step 2 n - 1
     if (ok) {
       tc_fence_after();
       const float inv = sum == 0.f ? 0.f : __int_as_float((127 - kBits) << 23) / sum;
