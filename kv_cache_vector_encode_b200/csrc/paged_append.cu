@@ -1,15 +1,29 @@
 // Append of new keys and values to the paged packed cache (tq_paged_append).
 //
 // Per vector: the key is turned to its position (rope.cu's formula, unrounded), then
-//   n = |x|, y = Pi x / n, idx_i = #{k : t_k < y_i}                      (Algorithm 1)
-//   r = x / n - Pi^T c[idx], gamma = |r|, z_i = [(S r)_i >= 0]             (Algorithm 2, values)
+//   n = |x|, u = x / n, y = Pi u, idx_i = #{k : t_k < y_i}               (Algorithm 1)
+//   r = u - Pi^T c[idx], gamma = |r|, z_i = [(S r)_i >= 0]                (Algorithm 2, values)
 // and the record goes to the token's slot.
+//
+// Up to three dependent d x d products per vector, 128 vectors at a time on the tensor cores. fp16 operands are split,
+// a = a_hi + 2^-12 a_lo, and three of the four partial products kept (what is left out is 2^-22 of the operands'
+// lengths), which with fp32 accumulation gives y and r to about 2^-19 at worst. That decides all but a few
+// coordinates as fp64 would. The others are known, since they lie within a band around a boundary that is wider
+// than the error, and are decided again by the whole warp with fp64 sums: about one in 10^4.
+// (All in fp64 on the SIMT cores, the first form of this kernel, took 1279 us for 8192 tokens of 8 heads.)
+//
+// Layout: a CTA takes tiles of 128 vectors (keys or values of consecutive heads and tokens), thread = (vector, group of
+// 32 coordinates), so that a thread packs a group's code words by itself. Products have the vectors as M (TMEM
+// lane = vector). Pi and S are resident in shared memory as K-major images of their rows; Pi^T c takes the same
+// image of Pi as an operand with the other major order, so that no transposed copy is needed.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
 
+#include "quant_device.cuh"
 #include "sm100.cuh"
 #include "tq_internal.h"
 
@@ -19,6 +33,7 @@ namespace {
 struct AppendParams {
   int64_t tokens, n_pos, slots_total, k_stride, v_stride;
   int Hkv, page_shift, half, pairs, f32;
+  int tiles;                   // tiles of 128 vectors, of the values and again of the keys
   const void* k;
   const void* v;
   const int64_t* slots;
@@ -26,6 +41,9 @@ struct AppendParams {
   const float2* table;
   const float* Pi;
   const float* S;
+  const float* T;              // S Pi^T
+  const uint8_t* pi_hi;        // shared-memory images of Pi's rows
+  const uint8_t* pi_lo;
   uint32_t* k_codes;
   uint16_t* k_norms;
   uint32_t* v_codes;
@@ -33,153 +51,438 @@ struct AppendParams {
   uint16_t* v_norms;
   uint16_t* v_gammas;
   int kb, vb;
-  float ck[16], tk[16], cv[16], tv[16];
+  float tk[16], cv[16], tv[16];
   uint32_t* err;
 };
 
-// A token's slot and position, checked; slot < 0 where nothing is to be written.
-__device__ __forceinline__ int64_t append_slot(const AppendParams& p, int64_t t, int32_t& pos) {
-  const int64_t slot = p.slots[t];
-  pos = p.half ? p.positions[t] : 0;
-  if (slot < 0) return -1;
-  if (slot >= p.slots_total || (p.half && (pos < 0 || pos >= p.n_pos))) {
-    atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
-    return -1;
-  }
-  return slot;
-}
-
-// Few tokens: everything in fp64 on the SIMT cores, one thread per coordinate and VPB vectors per block.
-// Three dependent passes over a d x d matrix (one for keys); with a few vectors per SM their latency is
-// the time, whatever the arithmetic.
-constexpr int kVpb = 4;
+constexpr int kVec = 128;              // vectors of a tile
+// |error of y| stays below 2^-18.4: 3 2^-22 for the splits, and 16 2^-23 should every step of the fp32
+// accumulation lose a whole unit (the sums stay below 1)
+constexpr float kBandY = 3.8146973e-6f;   // 2^-18
+// s = S r takes the error of r times up to |S_i|; decided again by |s| < band
+constexpr float kBandS = 1.2207031e-4f;   // 2^-13
+constexpr float kResScale = 8192.f;    // 2^13: |r| < 4 keeps fp16 in range
 
 template <int D>
-__device__ __forceinline__ void block_sum(double (&v)[kVpb], double (*red)[D / 32]) {
-#pragma unroll
-  for (int u = 0; u < kVpb; ++u) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
-    if ((threadIdx.x & 31) == 0) red[u][threadIdx.x >> 5] = v[u];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < kVpb; ++u) {
-    v[u] = 0.0;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) v[u] += red[u][w];
-  }
-  __syncthreads();
-}
+struct AppendLayout {
+  static constexpr uint32_t G = D / 32, kImg = kVec * D * 2, kMat = 128u * D * 2;
+  static constexpr uint32_t kPiHi = 0, kPiLo = kMat, kSHi = 2 * kMat, kSLo = 3 * kMat, kOpHi = 4 * kMat, kOpLo = kOpHi + kImg,
+                            kPart = kOpLo + kImg, kNorm = kPart + G * kVec * 8, kCode = kNorm + kVec * 8,
+                            kBar = kCode + kVec * G * 16, kTotal = kBar + 64 + 1024;
+};
 
 template <int D>
-__global__ void __launch_bounds__(D) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int G = D / 32;
-  __shared__ double sv[kVpb][D];
-  __shared__ double red[kVpb][G];
-  const bool value = blockIdx.y == 1;
-  const bool alg2 = value && p.v_signs;
-  const int i = threadIdx.x, g = i >> 5, lane = i & 31;
-  const int64_t v0 = (int64_t)blockIdx.x * kVpb, nv = p.tokens * p.Hkv;
-  int64_t rec[kVpb];
-  double x[kVpb], n[kVpb];
+struct AppendTile {
+  const AppendParams& p;
+  int64_t v0;                          // first vector
+  bool value;
+  __device__ __forceinline__ double raw(int64_t base, int e) const {
+    return p.f32 ? (double)((const float*)(value ? p.v : p.k))[base + e]
+                 : (double)__uint_as_float((uint32_t)((const uint16_t*)(value ? p.v : p.k))[base + e] << 16);
+  }
+  // element e of vector v of the tile (turned), as fp64: for the coordinates that are decided again
+  __device__ __forceinline__ double elem(int v, int e) const {
+    const int64_t t = (v0 + v) / p.Hkv;
+    const int64_t base = t * (value ? p.v_stride : p.k_stride) + ((v0 + v) - t * p.Hkv) * D;
+    const double x = raw(base, e);
+    if (value || e >= 2 * p.half) return x;
+    const int pair = p.pairs ? e >> 1 : (e < p.half ? e : e - p.half);
+    const bool second = p.pairs ? e & 1 : e >= p.half;
+    const float2 cs = p.table[(int64_t)p.positions[t] * p.half + pair];
+    const double o = raw(base, p.pairs ? e ^ 1 : (second ? e - p.half : e + p.half));
+    return second ? x * cs.x + o * cs.y : x * cs.x - o * cs.y;
+  }
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
-  for (int u = 0; u < kVpb; ++u) {
-    rec[u] = -1;
-    x[u] = 0.0;
-    if (v0 + u >= nv) continue;
-    const int64_t t = (v0 + u) / p.Hkv;
-    const int h = (int)((v0 + u) - t * p.Hkv);
-    int32_t pos;
-    const int64_t slot = append_slot(p, t, pos);
-    if (slot < 0) continue;
-    rec[u] = (((slot >> p.page_shift) * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-    const int64_t at = t * (value ? p.v_stride : p.k_stride) + (int64_t)h * D;
-    const void* src = value ? p.v : p.k;
-    auto elem = [&](int e) -> double {
-      return p.f32 ? (double)((const float*)src)[at + e] : (double)__uint_as_float((uint32_t)((const uint16_t*)src)[at + e] << 16);
-    };
-    x[u] = elem(i);
-    if (!value && i < 2 * p.half) {
-      const int pair = p.pairs ? i >> 1 : (i < p.half ? i : i - p.half);
-      const bool second = p.pairs ? i & 1 : i >= p.half;
-      const float2 cs = p.table[(int64_t)pos * p.half + pair];
-      const double o = elem(p.pairs ? i ^ 1 : (second ? i - p.half : i + p.half));
-      x[u] = second ? x[u] * cs.x + o * cs.y : x[u] * cs.x - o * cs.y;
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// fp16 parts of eight values into the operand images.
+__device__ __forceinline__ void split8(const float (&x)[8], uint8_t* hi, uint8_t* lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 a = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    const float2 b = __half22float2(a);
+    h[i] = h2_bits(a);
+    l[i] = h2_bits(__floats2half2_rn((x[2 * i] - b.x) * kSplitScale, (x[2 * i + 1] - b.y) * kSplitScale));
+  }
+  *(uint4*)hi = make_uint4(h[0], h[1], h[2], h[3]);
+  *(uint4*)lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Index of y: #{t < y} for the symmetric boundaries (P the positive ones), and whether y is within the band of one.
+template <int BITS>
+__device__ __forceinline__ int index_of(float y, const float (&P)[8], bool& near) {
+  const float a = fabsf(y);
+  const int m = sym_m<BITS>(a + kBandY, P);
+  near = a < kBandY || m != sym_m<BITS>(a - kBandY, P);
+  constexpr int H = 1 << (BITS - 1);
+  return y > 0.f ? H + m : H - 1 - m;
+}
+
+// Code words of a thread's 32 coordinates from the two accumulators (columns at, at + 128), y = (a + 2^-12 b) inv.
+template <int BITS>
+__device__ __forceinline__ uint32_t code_words(uint32_t at, float inv, const float (&P)[8], uint32_t (&words)[4]) {
+  uint32_t near = 0;
+#pragma unroll
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t a[16], b[16];
+    tmem_ld16(at + c, a);
+    tmem_ld16(at + 128 + c, b);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      bool close;
+      const int idx = index_of<BITS>(fmaf(__uint_as_float(b[k]), kSplitScaleInv, __uint_as_float(a[k])) * inv, P, close);
+#pragma unroll
+      for (int i = 0; i < BITS; ++i) words[i] |= (uint32_t)((idx >> i) & 1) << (c + k);
+      near |= (uint32_t)close << (c + k);
     }
   }
-#pragma unroll
-  for (int u = 0; u < kVpb; ++u) n[u] = x[u] * x[u];
-  block_sum<D>(n, red);
-  bool ok[kVpb];
-#pragma unroll
-  for (int u = 0; u < kVpb; ++u) {
-    n[u] = sqrt(n[u]);
-    ok[u] = n[u] > 0.0 && n[u] <= 1.7976931348623157e308;
-    x[u] = ok[u] ? x[u] / n[u] : 0.0;
-    sv[u][i] = x[u];
+  return near;
+}
+
+template <int D>
+__global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant__ AppendParams p) {
+  using L = AppendLayout<D>;
+  constexpr int G = D / 32, NT = kVec * G;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  double* part = (double*)(smem + L::kPart);                     // [G][128] partial sums of squares
+  double* norm = (double*)(smem + L::kNorm);                     // [128]
+  uint32_t* codes = (uint32_t*)(smem + L::kCode);                // [128][G][4] code words
+  uint64_t* bar = (uint64_t*)(smem + L::kBar);                   // Pi loaded, products done
+  uint32_t* tmem_slot = (uint32_t*)(bar + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int v = (warp & 3) * 32 + lane, g = warp >> 2;           // this thread's vector and group
+  if (tid == 0) {
+    mbar_init(&bar[0], 1);
+    mbar_init(&bar[1], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
   }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  // acc[u] = sum_j M[i][j] sv[u][j]
-  auto rows_product = [&](const float* M, double (&acc)[kVpb]) {
-    const float4* row = (const float4*)(M + (size_t)i * D);
-#pragma unroll 4
-    for (int j = 0; j < D / 4; ++j) {
-      const float4 m = __ldg(row + j);
+  tc_fence_after();
+  const uint32_t tacc = *tmem_slot, mine = tacc + ((uint32_t)((warp & 3) * 32) << 16) + g * 32;
+  if (tid == 0) {                                                // at d = 64 the images' first column block
+    mbar_arrive_expect_tx(&bar[0], 2 * L::kMat);
+    bulk_g2s(smem + L::kPiHi, p.pi_hi, L::kMat, &bar[0]);
+    bulk_g2s(smem + L::kPiLo, p.pi_lo, L::kMat, &bar[0]);
+  }
+  bool loaded = false, have_s = false;
+  uint32_t phase = 0;
+  // one product of the operand with a resident matrix (B = its rows, or its columns), into both accumulators
+  auto product = [&](uint32_t mat, bool columns) -> bool {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0 && elect_one_sync()) {
+      const uint32_t mh = smem_u32(smem + mat), ml = mh + L::kMat, xh = smem_u32(smem + L::kOpHi), xl = xh + L::kImg;
 #pragma unroll
-      for (int u = 0; u < kVpb; ++u) {
-        acc[u] = fma((double)m.x, sv[u][4 * j], acc[u]);
-        acc[u] = fma((double)m.y, sv[u][4 * j + 1], acc[u]);
-        acc[u] = fma((double)m.z, sv[u][4 * j + 2], acc[u]);
-        acc[u] = fma((double)m.w, sv[u][4 * j + 3], acc[u]);
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
+        const uint64_t dh = desc_kmajor_sw128(xh + at), dl = desc_kmajor_sw128(xl + at);
+        if (columns) {
+          // B[n][k] = M[k][n]: 16 rows (2048 bytes) of the image per step, 64 columns per block
+#pragma unroll
+          for (int nb = 0; nb < D / 64; ++nb) {
+            const uint32_t idesc = idesc_f16_f32(128, 64) | (1u << 16), b = nb * 16384u + ks * 2048u;
+            const uint64_t bh = desc_smem(mh + b, 1024, 1024, 2), bl = desc_smem(ml + b, 1024, 1024, 2);
+            mma_f16_ss(tacc + 64 * nb, dh, bh, idesc, ks > 0);
+            mma_f16_ss(tacc + 128 + 64 * nb, dh, bl, idesc, ks > 0);
+            mma_f16_ss(tacc + 128 + 64 * nb, dl, bh, idesc, 1);
+          }
+        } else {
+          const uint32_t idesc = idesc_f16_f32(128, D);
+          const uint64_t bh = desc_kmajor_sw128(mh + at), bl = desc_kmajor_sw128(ml + at);
+          mma_f16_ss(tacc, dh, bh, idesc, ks > 0);
+          mma_f16_ss(tacc + 128, dh, bl, idesc, ks > 0);
+          mma_f16_ss(tacc + 128, dl, bh, idesc, 1);
+        }
+      }
+      mma_commit(&bar[1]);
+    }
+    __syncwarp();
+    const bool ok = __syncthreads_and(mbar_wait(&bar[1], phase, p.err, kDevTimeoutMma, abort_flag));
+    phase ^= 1;
+    tc_fence_after();
+    return ok;
+  };
+
+  for (int item = blockIdx.x; item < 2 * p.tiles; item += gridDim.x) {
+    const bool value = item < p.tiles, alg2 = value && p.v_signs;
+    const AppendTile<D> tile{p, (int64_t)(value ? item : item - p.tiles) * kVec, value};
+    const int64_t t = (tile.v0 + v) / p.Hkv;
+    const int h = (int)((tile.v0 + v) - t * p.Hkv);
+    // ---- the vector's 32 coordinates, through shared memory for the partners of the turn ------------------
+    int64_t rec = -1;
+    int pos = 0;
+    if (t < p.tokens) {
+      const int64_t slot = p.slots[t];
+      pos = p.half ? p.positions[t] : 0;
+      if (slot >= p.slots_total || (slot >= 0 && p.half && (pos < 0 || pos >= p.n_pos)))
+        atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+      else if (slot >= 0)
+        rec = (((slot >> p.page_shift) * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+    }
+    float x[32];
+    {
+      const int64_t base = t * (value ? p.v_stride : p.k_stride) + (int64_t)h * D + g * 32;
+      if (rec < 0) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = 0.f;
+      } else if (p.f32) {
+        const float4* src = (const float4*)((const float*)(value ? p.v : p.k) + base);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 w = __ldg(src + k);
+          x[4 * k] = w.x, x[4 * k + 1] = w.y, x[4 * k + 2] = w.z, x[4 * k + 3] = w.w;
+        }
+      } else {
+        const uint4* src = (const uint4*)((const uint16_t*)(value ? p.v : p.k) + base);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 w = __ldg(src + k);
+          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[8 * k + 2 * i] = __uint_as_float(q[i] << 16);
+            x[8 * k + 2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+          }
+        }
       }
     }
-  };
-  double y[kVpb] = {};
-  rows_product(p.Pi, y);
-  __syncthreads();
-  const int bits = value ? p.vb : p.kb, L = 1 << bits;
-  const float* tab = value ? p.tv : p.tk;
-  uint32_t* codes = value ? p.v_codes : p.k_codes;
-  uint16_t* norms = value ? p.v_norms : p.k_norms;
+    double ss = 0.0;
+    if (!value && p.half) {                                      // uniform over the block
+      float* raw = (float*)(smem + L::kOpHi);                    // [coordinate][vector]
 #pragma unroll
-  for (int u = 0; u < kVpb; ++u) {
-    int idx = 0;
-    for (int k = 0; k < L - 1; ++k) idx += (double)tab[k] < y[u] ? 1 : 0;
-    for (int b = 0; b < bits; ++b) {
-      const uint32_t w = __ballot_sync(0xffffffffu, (idx >> b) & 1);
-      if (lane == 0 && rec[u] >= 0) codes[(rec[u] * G + g) * bits + b] = w;
+      for (int k = 0; k < 32; ++k) raw[(g * 32 + k) * kVec + v] = x[k];
+      __syncthreads();
+      const float2* row = p.table + (int64_t)(rec < 0 ? 0 : pos) * p.half;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const int e = g * 32 + k;
+        double y = (double)x[k];
+        if (e < 2 * p.half && rec >= 0) {
+          const int pair = p.pairs ? e >> 1 : (e < p.half ? e : e - p.half);
+          const bool second = p.pairs ? e & 1 : e >= p.half;
+          const float2 cs = __ldg(row + pair);
+          const double o = (double)raw[(p.pairs ? e ^ 1 : (second ? e - p.half : e + p.half)) * kVec + v];
+          y = second ? y * cs.x + o * cs.y : y * cs.x - o * cs.y;
+        }
+        ss = fma(y, y, ss);
+        x[k] = (float)y;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) ss = fma((double)x[k], (double)x[k], ss);
     }
-    if (i == 0 && rec[u] >= 0) norms[rec[u]] = __half_as_ushort(__double2half(n[u]));
-    if (alg2) sv[u][i] = (double)p.cv[idx];
+    part[g * kVec + v] = ss;
+    __syncthreads();
+    ss = 0.0;
+#pragma unroll
+    for (int k = 0; k < G; ++k) ss += part[k * kVec + v];
+    const double n = sqrt(ss);
+    const bool ok = n > 0.0 && n <= 1.7976931348623157e308;
+    if (g == 0) norm[v] = n;
+    // ---- y = Pi x: x times a power of two, |x| in [2^14, 2^15) ---------------------------------------------
+    float f1 = 0.f, f2 = 0.f, inv = 0.f;
+    if (ok) {
+      int E;
+      frexp(n, &E);
+      pow2_pair(15 - E, f1, f2);
+      inv = (float)(1.0 / ldexp(n, 15 - E));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = x[8 * c + k] = ok ? x[8 * c + k] * f1 * f2 : 0.f;
+      const uint32_t off = sw128_offset(v, (g * 32 + c * 8) * 2, kVec);
+      split8(w, smem + L::kOpHi + off, smem + L::kOpLo + off);
+    }
+    if (!loaded) {
+      if (!__syncthreads_and(mbar_wait(&bar[0], 0, p.err, kDevTimeoutLoad, abort_flag))) break;
+      loaded = true;
+    }
+    if (alg2 && !have_s) {                                       // S into its images, once
+      for (int e = tid; e < D * D / 8; e += NT) {
+        const int r = e / (D / 8), c = e % (D / 8);
+        const float4 a = __ldg((const float4*)(p.S + (size_t)r * D) + 2 * c), b = __ldg((const float4*)(p.S + (size_t)r * D) + 2 * c + 1);
+        const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t off = sw128_offset(r, c * 16, 128);
+        split8(w, smem + L::kSHi + off, smem + L::kSLo + off);
+      }
+      have_s = true;
+    }
+    if (!product(L::kPiHi, false)) break;
+    // ---- indices --------------------------------------------------------------------------------------------
+    const int bits = value ? p.vb : p.kb;
+    uint32_t words[4] = {0, 0, 0, 0}, near;
+    {
+      float P[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = (1 << (bits - 1)) + k;                    // boundary 2^(bits-1) is the first positive one
+        P[k] = at < (1 << bits) - 1 ? (value ? p.tv[at] : p.tk[at]) : INFINITY;
+      }
+      near = bits == 1   ? code_words<1>(mine, inv, P, words)
+             : bits == 2 ? code_words<2>(mine, inv, P, words)
+             : bits == 3 ? code_words<3>(mine, inv, P, words)
+                         : code_words<4>(mine, inv, P, words);
+    }
+    // a turned key outside the fp32 range has no operand to speak of: all its coordinates in fp64
+    if (!value && p.half && (n < 1.2e-38 || n > 3.3e38)) near = ~0u;
+    if (!ok || rec < 0) near = 0;                                // y is exactly zero
+    const float* tab = value ? p.tv : p.tk;
+    for (uint32_t who; (who = __ballot_sync(0xffffffffu, near != 0)) != 0;) {
+      const int src = __ffs(who) - 1, vv = (warp & 3) * 32 + src;
+      const int k = __ffs(__shfl_sync(0xffffffffu, near, src)) - 1, i = g * 32 + k;
+      double d = 0.0;
+#pragma unroll
+      for (int j = lane; j < D; j += 32) d = fma((double)__ldg(p.Pi + (size_t)i * D + j), tile.elem(vv, j), d);
+      const double y = warp_sum(d) / norm[vv];
+      int idx = 0;
+      for (int b = 0; b < (1 << bits) - 1; ++b) idx += (double)tab[b] < y ? 1 : 0;
+      if (lane == src) {
+        near &= near - 1;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (b < bits) words[b] = (words[b] & ~(1u << k)) | (uint32_t)((idx >> b) & 1) << k;
+      }
+    }
+    if (rec >= 0) {
+      uint32_t* dst = (value ? p.v_codes : p.k_codes) + (rec * G + g) * bits;
+      for (int b = 0; b < bits; ++b) dst[b] = words[b];
+      if (g == 0) (value ? p.v_norms : p.k_norms)[rec] = __half_as_ushort(__double2half(n));
+    }
+    if (!alg2) {
+      tc_fence_before();
+      __syncthreads();                                           // norms and records are read
+      continue;
+    }
+    // ---- Pi^T c[idx] -----------------------------------------------------------------------------------------
+#pragma unroll
+    for (int b = 0; b < 4; ++b) codes[(v * G + g) * 4 + b] = words[b];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = 8 * c + k;
+        const int idx = ((words[0] >> at) & 1) | ((words[1] >> at) & 1) << 1 | ((words[2] >> at) & 1) << 2;
+        w[k] = p.cv[idx] * kSplitScale;
+      }
+      const uint32_t off = sw128_offset(v, (g * 32 + c * 8) * 2, kVec);
+      split8(w, smem + L::kOpHi + off, smem + L::kOpLo + off);
+    }
+    if (!product(L::kPiHi, true)) break;
+    // ---- r = u - Pi^T c, gamma ---------------------------------------------------------------------------------
+    double gs = 0.0;
+#pragma unroll
+    for (int c = 0; c < 32; c += 16) {
+      uint32_t a[16], b[16];
+      tmem_ld16(mine + c, a);
+      tmem_ld16(mine + 128 + c, b);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float e = fmaf(__uint_as_float(b[k]), kSplitScaleInv, __uint_as_float(a[k])) * kSplitScaleInv;
+        x[c + k] = ok ? fmaf(x[c + k], inv, -e) : 0.f;
+        gs = fma((double)x[c + k], (double)x[c + k], gs);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = x[8 * c + k] * kResScale;
+      const uint32_t off = sw128_offset(v, (g * 32 + c * 8) * 2, kVec);
+      split8(w, smem + L::kOpHi + off, smem + L::kOpLo + off);
+    }
+    part[g * kVec + v] = gs;
+    if (!product(L::kSHi, false)) break;
+    // ---- signs -------------------------------------------------------------------------------------------------
+    uint32_t sign = 0;
+    near = 0;
+#pragma unroll
+    for (int c = 0; c < 32; c += 16) {
+      uint32_t a[16], b[16];
+      tmem_ld16(mine + c, a);
+      tmem_ld16(mine + 128 + c, b);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float s = fmaf(__uint_as_float(b[k]), kSplitScaleInv, __uint_as_float(a[k]));
+        sign |= (uint32_t)(s >= 0.f) << (c + k);
+        near |= (uint32_t)(fabsf(s) < kBandS * kResScale) << (c + k);
+      }
+    }
+    if (!ok || rec < 0) near = 0;                                // r is exactly zero
+    for (uint32_t who; (who = __ballot_sync(0xffffffffu, near != 0)) != 0;) {
+      const int src = __ffs(who) - 1, vv = (warp & 3) * 32 + src;
+      const int k = __ffs(__shfl_sync(0xffffffffu, near, src)) - 1, i = g * 32 + k;
+      // (S r)_i = S_i u - T_i c in fp64. T is rounded to fp32: off by 2^-24 |T_i| |c| at most
+      double su = 0.0, tc = 0.0, tt = 0.0, cc = 0.0;
+      for (int j = lane; j < D; j += 32) {
+        const uint32_t* w = codes + (vv * G + (j >> 5)) * 4;
+        const int at = j & 31, idx = ((w[0] >> at) & 1) | ((w[1] >> at) & 1) << 1 | ((w[2] >> at) & 1) << 2;
+        const double tij = (double)__ldg(p.T + (size_t)i * D + j), cj = (double)p.cv[idx];
+        su = fma((double)__ldg(p.S + (size_t)i * D + j), tile.elem(vv, j), su);
+        tc = fma(tij, cj, tc);
+        tt = fma(tij, tij, tt);
+        cc = fma(cj, cj, cc);
+      }
+      const double un = 1.0 / norm[vv];
+      su = warp_sum(su);
+      double s = su * un - warp_sum(tc);
+      tt = warp_sum(tt);
+      cc = warp_sum(cc);
+      if (fabs(s) <= 6e-8 * sqrt(tt * cc) + 1e-12) {             // still undecided: T_i from S and Pi themselves
+        s = 0.0;
+        for (int j = 0; j < D; ++j) {
+          double a = 0.0;
+          for (int q = lane; q < D; q += 32) {
+            const uint32_t* w = codes + (vv * G + (q >> 5)) * 4;
+            const int at = q & 31, idx = ((w[0] >> at) & 1) | ((w[1] >> at) & 1) << 1 | ((w[2] >> at) & 1) << 2;
+            a = fma((double)__ldg(p.Pi + (size_t)q * D + j), (double)p.cv[idx], a);
+          }
+          s = fma((double)__ldg(p.S + (size_t)i * D + j), tile.elem(vv, j) / norm[vv] - warp_sum(a), s);
+        }
+      }
+      if (lane == src) {
+        near &= near - 1;
+        sign = (sign & ~(1u << k)) | (uint32_t)(s >= 0.0) << k;
+      }
+    }
+    if (rec >= 0) {
+      p.v_signs[rec * G + g] = sign;
+      if (g == 0) {
+        gs = 0.0;
+#pragma unroll
+        for (int k = 0; k < G; ++k) gs += part[k * kVec + v];
+        p.v_gammas[rec] = __half_as_ushort(__double2half(sqrt(gs)));
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
   }
-  if (!alg2) return;
+  if (tid == 0 && !loaded) mbar_wait(&bar[0], 0, p.err, kDevTimeoutLoad, abort_flag);   // no copy outlives the block
+  tc_fence_before();
   __syncthreads();
-  double a[kVpb] = {};
-#pragma unroll 4
-  for (int j = 0; j < D; ++j) {
-    const double m = (double)__ldg(p.Pi + (size_t)j * D + i);
-#pragma unroll
-    for (int u = 0; u < kVpb; ++u) a[u] = fma(m, sv[u][j], a[u]);
-  }
-  __syncthreads();
-  double ga[kVpb];
-#pragma unroll
-  for (int u = 0; u < kVpb; ++u) {
-    const double r = ok[u] ? x[u] - a[u] : 0.0;
-    sv[u][i] = r;
-    ga[u] = r * r;
-  }
-  block_sum<D>(ga, red);
-  double s[kVpb] = {};
-  rows_product(p.S, s);
-#pragma unroll
-  for (int u = 0; u < kVpb; ++u) {
-    const uint32_t w = __ballot_sync(0xffffffffu, s[u] >= 0.0);
-    if (rec[u] < 0) continue;
-    if (lane == 0) p.v_signs[rec[u] * G + g] = w;
-    if (i == 0) p.v_gammas[rec[u]] = __half_as_ushort(__double2half(sqrt(ga[u])));
-  }
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tacc, 256);
 }
 
 }  // namespace
@@ -228,6 +531,9 @@ extern "C" TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t token
   p.table = (const float2*)table;
   p.Pi = (const float*)((const uint8_t*)rot + RL.pi32);
   p.S = (const float*)((const uint8_t*)rot + RL.s32);
+  p.T = (const float*)((const uint8_t*)rot + RL.t32);
+  p.pi_hi = (const uint8_t*)rot + RL.pi_hi;
+  p.pi_lo = (const uint8_t*)rot + RL.pi_lo;
   p.k_codes = kv->k_codes;
   p.k_norms = kv->k_norms;
   p.v_codes = kv->v_codes;
@@ -237,18 +543,21 @@ extern "C" TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t token
   p.kb = kv->k_bits;
   p.vb = kv->v_bits;
   for (int k = 0; k < 16; ++k) {
-    p.ck[k] = kv->ck[k];
     p.tk[k] = kv->tk[k];
     p.cv[k] = kv->cv[k];
     p.tv[k] = kv->tv[k];
   }
   p.err = device_error_word();
   if (!p.err) return fail(TQ_ERR_CUDA, f + ": no device error word (is a CUDA device present?)");
-  const dim3 grid((unsigned)((tokens * kv->Hkv + kVpb - 1) / kVpb), 2);
-  if (kv->d == 128)
-    append_kernel<128><<<grid, 128, 0, (cudaStream_t)stream>>>(p);
-  else
-    append_kernel<64><<<grid, 64, 0, (cudaStream_t)stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_append: launch");
+  const int tiles = (int)((tokens * kv->Hkv + kVec - 1) / kVec);
+  p.tiles = tiles;
+  const unsigned grid = (unsigned)std::min(2 * tiles, sm_count());
+  auto go = [&](auto kern, int smem, int threads) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "tq_paged_append: shared memory attribute");
+    kern<<<grid, threads, smem, (cudaStream_t)stream>>>(p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_append: launch");
+  };
+  return kv->d == 128 ? go(append_kernel<128>, AppendLayout<128>::kTotal, 512) : go(append_kernel<64>, AppendLayout<64>::kTotal, 256);
 }
