@@ -42,8 +42,7 @@ struct AppendParams {
   const float* Pi;
   const float* S;
   const float* T;              // S Pi^T
-  const uint8_t* pi_hi;        // shared-memory images of Pi's rows
-  const uint8_t* pi_lo;
+  const uint8_t* img[4];       // shared-memory images of the rows of Pi and S: high and low parts of each
   uint32_t* k_codes;
   uint16_t* k_norms;
   uint32_t* v_codes;
@@ -56,9 +55,12 @@ struct AppendParams {
 };
 
 constexpr int kVec = 128;              // vectors of a tile
-// |error of y| stays below 2^-18.4: 3 2^-22 for the splits, and 16 2^-23 should every step of the fp32
-// accumulation lose a whole unit (the sums stay below 1)
+// |error of y| stays below 3.1e-6: 3 2^-22 for the splits, 16 2^-23 should every step of the fp32 accumulation lose a whole
+// unit (the sums stay below 1), and 2^-21.3 of y for the length: sums of eight squares of turned coordinates (3 2^-24)
+// and their sum, halved by the root
 constexpr float kBandY = 3.8146973e-6f;   // 2^-18
+// the length itself is rounded to fp16 only where 2^-20 of it makes no difference
+constexpr float kBandN = 9.5367432e-7f;   // 2^-20
 // s = S r takes the error of r times up to |S_i|; decided again by |s| < band
 constexpr float kBandS = 1.2207031e-4f;   // 2^-13
 constexpr float kResScale = 8192.f;    // 2^13: |r| < 4 keeps fp16 in range
@@ -66,9 +68,9 @@ constexpr float kResScale = 8192.f;    // 2^13: |r| < 4 keeps fp16 in range
 template <int D>
 struct AppendLayout {
   static constexpr uint32_t G = D / 32, kImg = kVec * D * 2, kMat = 128u * D * 2;
-  static constexpr uint32_t kPiHi = 0, kPiLo = kMat, kSHi = 2 * kMat, kSLo = 3 * kMat, kOpHi = 4 * kMat, kOpLo = kOpHi + kImg,
-                            kPart = kOpLo + kImg, kNorm = kPart + G * kVec * 8, kCode = kNorm + kVec * 8,
-                            kBar = kCode + kVec * G * 16, kTotal = kBar + 64 + 1024;
+  static constexpr uint32_t kPiHi = 0, kSHi = 2 * kMat, kOpHi = 4 * kMat, kOpLo = kOpHi + kImg,
+                            kPart = kOpLo + kImg, kTop = kPart + G * kVec * 4, kCode = kTop + G * kVec * 4,
+                            kLevel = kCode + kVec * G * 16, kBar = kLevel + 64, kTotal = kBar + 64 + 1024;
 };
 
 template <int D>
@@ -146,26 +148,65 @@ __device__ __forceinline__ uint32_t code_words(uint32_t at, float inv, const flo
   return near;
 }
 
-template <int D>
+// What a thread fetches of an item: its vector's record number and 32 coordinates, as they come.
+struct AppendFetch {
+  int64_t rec;                 // -1: nothing to write
+  int pos;
+  uint4 raw[8];
+};
+
+template <int D, bool F32>
 __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant__ AppendParams p) {
   using L = AppendLayout<D>;
-  constexpr int G = D / 32, NT = kVec * G;
+  constexpr int G = D / 32, NR = F32 ? 8 : 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  double* part = (double*)(smem + L::kPart);                     // [G][128] partial sums of squares
-  double* norm = (double*)(smem + L::kNorm);                     // [128]
+  float* part = (float*)(smem + L::kPart);                       // [G][128] partial sums of squares
+  uint32_t* top = (uint32_t*)(smem + L::kTop);                   // [G][128] largest magnitudes (as integers)
   uint32_t* codes = (uint32_t*)(smem + L::kCode);                // [128][G][4] code words
-  uint64_t* bar = (uint64_t*)(smem + L::kBar);                   // Pi loaded, products done
+  uint32_t* level = (uint32_t*)(smem + L::kLevel);               // [8] fp16 parts of 2^12 c: high, low
+  uint64_t* bar = (uint64_t*)(smem + L::kBar);                   // matrices loaded, products done
   uint32_t* tmem_slot = (uint32_t*)(bar + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int v = (warp & 3) * 32 + lane, g = warp >> 2;           // this thread's vector and group
+  const bool with_s = p.v_signs && (int)blockIdx.x < p.tiles;    // some item of this CTA needs S
   if (tid == 0) {
     mbar_init(&bar[0], 1);
     mbar_init(&bar[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
+    mbar_arrive_expect_tx(&bar[0], (with_s ? 4 : 2) * L::kMat);  // at d = 64 the images' first column block
+    for (int i = 0; i < (with_s ? 4 : 2); ++i) bulk_g2s(smem + i * L::kMat, p.img[i], L::kMat, &bar[0]);
   }
+  if (tid < 8) {
+    const float c = p.cv[tid] * kSplitScale;
+    const __half h = __float2half_rn(c);
+    level[tid] = (uint32_t)__half_as_ushort(h) | (uint32_t)__half_as_ushort(__float2half_rn((c - __half2float(h)) * kSplitScale)) << 16;
+  }
+  auto fetch = [&](int item, AppendFetch& f) {
+    f.rec = -1;
+    f.pos = 0;
+#pragma unroll
+    for (int k = 0; k < NR; ++k) f.raw[k] = make_uint4(0, 0, 0, 0);
+    if (item >= 2 * p.tiles) return;
+    const bool value = item < p.tiles;
+    const int64_t n = (int64_t)(value ? item : item - p.tiles) * kVec + v, t = n / p.Hkv;
+    if (t >= p.tokens) return;
+    const int h = (int)(n - t * p.Hkv);
+    const int64_t base = t * (value ? p.v_stride : p.k_stride) + (int64_t)h * D + g * 32;
+    const uint4* src = (const uint4*)((const uint8_t*)(value ? p.v : p.k) + base * (F32 ? 4 : 2));
+    const int64_t slot = p.slots[t];
+    f.pos = p.half ? p.positions[t] : 0;
+#pragma unroll
+    for (int k = 0; k < NR; ++k) f.raw[k] = __ldg(src + k);
+    if (slot >= p.slots_total || (slot >= 0 && p.half && (f.pos < 0 || f.pos >= p.n_pos)))
+      atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+    else if (slot >= 0)
+      f.rec = (((slot >> p.page_shift) * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+  };
+  AppendFetch in;
+  fetch(blockIdx.x, in);
   if (warp == 0) {
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
@@ -174,12 +215,7 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tacc = *tmem_slot, mine = tacc + ((uint32_t)((warp & 3) * 32) << 16) + g * 32;
-  if (tid == 0) {                                                // at d = 64 the images' first column block
-    mbar_arrive_expect_tx(&bar[0], 2 * L::kMat);
-    bulk_g2s(smem + L::kPiHi, p.pi_hi, L::kMat, &bar[0]);
-    bulk_g2s(smem + L::kPiLo, p.pi_lo, L::kMat, &bar[0]);
-  }
-  bool loaded = false, have_s = false;
+  bool loaded = false;
   uint32_t phase = 0;
   // one product of the operand with a resident matrix (B = its rows, or its columns), into both accumulators
   auto product = [&](uint32_t mat, bool columns) -> bool {
@@ -194,15 +230,12 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
         const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
         const uint64_t dh = desc_kmajor_sw128(xh + at), dl = desc_kmajor_sw128(xl + at);
         if (columns) {
-          // B[n][k] = M[k][n]: 16 rows (2048 bytes) of the image per step, 64 columns per block
-#pragma unroll
-          for (int nb = 0; nb < D / 64; ++nb) {
-            const uint32_t idesc = idesc_f16_f32(128, 64) | (1u << 16), b = nb * 16384u + ks * 2048u;
-            const uint64_t bh = desc_smem(mh + b, 1024, 1024, 2), bl = desc_smem(ml + b, 1024, 1024, 2);
-            mma_f16_ss(tacc + 64 * nb, dh, bh, idesc, ks > 0);
-            mma_f16_ss(tacc + 128 + 64 * nb, dh, bl, idesc, ks > 0);
-            mma_f16_ss(tacc + 128 + 64 * nb, dl, bh, idesc, 1);
-          }
+          // B[n][k] = M[k][n]: 16 rows (2048 bytes) of the image per step; 64 columns per block, blocks 16 KB apart
+          const uint32_t idesc = idesc_f16_f32(128, D) | (1u << 16);
+          const uint64_t bh = desc_smem(mh + ks * 2048u, 16384, 1024, 2), bl = desc_smem(ml + ks * 2048u, 16384, 1024, 2);
+          mma_f16_ss(tacc, dh, bh, idesc, ks > 0);
+          mma_f16_ss(tacc + 128, dh, bl, idesc, ks > 0);
+          mma_f16_ss(tacc + 128, dl, bh, idesc, 1);
         } else {
           const uint32_t idesc = idesc_f16_f32(128, D);
           const uint64_t bh = desc_kmajor_sw128(mh + at), bl = desc_kmajor_sw128(ml + at);
@@ -220,113 +253,91 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     return ok;
   };
 
+#pragma unroll 1
   for (int item = blockIdx.x; item < 2 * p.tiles; item += gridDim.x) {
     const bool value = item < p.tiles, alg2 = value && p.v_signs;
     const AppendTile<D> tile{p, (int64_t)(value ? item : item - p.tiles) * kVec, value};
-    const int64_t t = (tile.v0 + v) / p.Hkv;
-    const int h = (int)((tile.v0 + v) - t * p.Hkv);
-    // ---- the vector's 32 coordinates, through shared memory for the partners of the turn ------------------
-    int64_t rec = -1;
-    int pos = 0;
-    if (t < p.tokens) {
-      const int64_t slot = p.slots[t];
-      pos = p.half ? p.positions[t] : 0;
-      if (slot >= p.slots_total || (slot >= 0 && p.half && (pos < 0 || pos >= p.n_pos)))
-        atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
-      else if (slot >= 0)
-        rec = (((slot >> p.page_shift) * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-    }
+    const int64_t rec = in.rec;
     float x[32];
-    {
-      const int64_t base = t * (value ? p.v_stride : p.k_stride) + (int64_t)h * D + g * 32;
-      if (rec < 0) {
+    uint32_t most = 0;                                           // bits of the largest magnitude
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = 0.f;
-      } else if (p.f32) {
-        const float4* src = (const float4*)((const float*)(value ? p.v : p.k) + base);
+    for (int k = 0; k < NR; ++k) {
+      const uint32_t q[4] = {in.raw[k].x, in.raw[k].y, in.raw[k].z, in.raw[k].w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 w = __ldg(src + k);
-          x[4 * k] = w.x, x[4 * k + 1] = w.y, x[4 * k + 2] = w.z, x[4 * k + 3] = w.w;
+      for (int i = 0; i < 4; ++i) {
+        if (F32) {
+          x[4 * k + i] = __uint_as_float(q[i]);
+        } else {
+          x[8 * k + 2 * i] = __uint_as_float(q[i] << 16);
+          x[8 * k + 2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
         }
-      } else {
-        const uint4* src = (const uint4*)((const uint16_t*)(value ? p.v : p.k) + base);
+      }
+    }
+    // ---- turn, with the partners through shared memory ---------------------------------------------------------
+    if (!value && p.half) {                                      // uniform over the block
+      float* raw = (float*)(smem + L::kOpHi);                    // [coordinate][vector]
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 w = __ldg(src + k);
-          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+      for (int k = 0; k < 32; ++k) {
+        raw[(g * 32 + k) * kVec + v] = x[k];
+        most |= x[k] != 0.f ? 1u : 0u;
+      }
+      __syncthreads();
+      const float2* row = p.table + (int64_t)(rec < 0 ? 0 : in.pos) * p.half;
+      const int rot = 2 * p.half;
+      if (rec >= 0 && g * 32 < rot) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[8 * k + 2 * i] = __uint_as_float(q[i] << 16);
-            x[8 * k + 2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+        for (int k = 0; k < 32; ++k) {
+          const int e = g * 32 + k;
+          const int pair = p.pairs ? e >> 1 : (e < p.half ? e : e - p.half);
+          const bool second = p.pairs ? e & 1 : e >= p.half;
+          if (e < rot) {
+            const float2 cs = __ldg(row + pair);
+            const float o = raw[(p.pairs ? e ^ 1 : (second ? e - p.half : e + p.half)) * kVec + v];
+            x[k] = fmaf(x[k], cs.x, second ? o * cs.y : -(o * cs.y));
           }
         }
       }
     }
-    double ss = 0.0;
-    if (!value && p.half) {                                      // uniform over the block
-      float* raw = (float*)(smem + L::kOpHi);                    // [coordinate][vector]
 #pragma unroll
-      for (int k = 0; k < 32; ++k) raw[(g * 32 + k) * kVec + v] = x[k];
-      __syncthreads();
-      const float2* row = p.table + (int64_t)(rec < 0 ? 0 : pos) * p.half;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int e = g * 32 + k;
-        double y = (double)x[k];
-        if (e < 2 * p.half && rec >= 0) {
-          const int pair = p.pairs ? e >> 1 : (e < p.half ? e : e - p.half);
-          const bool second = p.pairs ? e & 1 : e >= p.half;
-          const float2 cs = __ldg(row + pair);
-          const double o = (double)raw[(p.pairs ? e ^ 1 : (second ? e - p.half : e + p.half)) * kVec + v];
-          y = second ? y * cs.x + o * cs.y : y * cs.x - o * cs.y;
-        }
-        ss = fma(y, y, ss);
-        x[k] = (float)y;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) ss = fma((double)x[k], (double)x[k], ss);
-    }
-    part[g * kVec + v] = ss;
+    for (int k = 0; k < 32; ++k) most = max(most, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+    top[g * kVec + v] = most;
     __syncthreads();
-    ss = 0.0;
 #pragma unroll
-    for (int k = 0; k < G; ++k) ss += part[k * kVec + v];
-    const double n = sqrt(ss);
-    const bool ok = n > 0.0 && n <= 1.7976931348623157e308;
-    if (g == 0) norm[v] = n;
-    // ---- y = Pi x: x times a power of two, |x| in [2^14, 2^15) ---------------------------------------------
-    float f1 = 0.f, f2 = 0.f, inv = 0.f;
+    for (int k = 0; k < G; ++k) most = max(most, top[k * kVec + v]);
+    // ---- y = Pi x: x times a power of two that brings its largest coordinate into [2^13, 2^14) -------------------
+    const bool ok = rec >= 0 && most > 0 && most < 0x7F800000u;  // a row that is zero or not finite: u = 0
+    // keys outside what fp32 turns well: above 5e37 (products may overflow) or below 1e-30 (they may be subnormal)
+    const bool far = rec >= 0 && !value && p.half && most > 0 && (most < 0x0DA24260u || most > 0x7E167699u);
+    float f1 = 0.f, f2 = 0.f;
+    int E = 0;
     if (ok) {
-      int E;
-      frexp(n, &E);
-      pow2_pair(15 - E, f1, f2);
-      inv = (float)(1.0 / ldexp(n, 15 - E));
+      frexpf(__uint_as_float(most), &E);
+      pow2_pair(14 - E, f1, f2);
     }
+    float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       float w[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = x[8 * c + k] = ok ? x[8 * c + k] * f1 * f2 : 0.f;
+      for (int k = 0; k < 8; ++k) {
+        w[k] = x[8 * c + k] = ok ? x[8 * c + k] * f1 * f2 : 0.f;
+        s4[c] = fmaf(w[k], w[k], s4[c]);
+      }
       const uint32_t off = sw128_offset(v, (g * 32 + c * 8) * 2, kVec);
       split8(w, smem + L::kOpHi + off, smem + L::kOpLo + off);
     }
+    part[g * kVec + v] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
     if (!loaded) {
       if (!__syncthreads_and(mbar_wait(&bar[0], 0, p.err, kDevTimeoutLoad, abort_flag))) break;
       loaded = true;
     }
-    if (alg2 && !have_s) {                                       // S into its images, once
-      for (int e = tid; e < D * D / 8; e += NT) {
-        const int r = e / (D / 8), c = e % (D / 8);
-        const float4 a = __ldg((const float4*)(p.S + (size_t)r * D) + 2 * c), b = __ldg((const float4*)(p.S + (size_t)r * D) + 2 * c + 1);
-        const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        const uint32_t off = sw128_offset(r, c * 16, 128);
-        split8(w, smem + L::kSHi + off, smem + L::kSLo + off);
-      }
-      have_s = true;
-    }
     if (!product(L::kPiHi, false)) break;
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < G; ++k) ss += part[k * kVec + v];
+    const float len = sqrtf(ss);                                 // |x| 2^(14 - E)
+    const float inv = ok ? 1.f / len : 0.f;
+    fetch(item + gridDim.x, in);                                 // the next item's, while this one goes on
     // ---- indices --------------------------------------------------------------------------------------------
     const int bits = value ? p.vb : p.kb;
     uint32_t words[4] = {0, 0, 0, 0}, near;
@@ -342,17 +353,22 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
              : bits == 3 ? code_words<3>(mine, inv, P, words)
                          : code_words<4>(mine, inv, P, words);
     }
-    // a turned key outside the fp32 range has no operand to speak of: all its coordinates in fp64
-    if (!value && p.half && (n < 1.2e-38 || n > 3.3e38)) near = ~0u;
-    if (!ok || rec < 0) near = 0;                                // y is exactly zero
+    near = far ? ~0u : ok ? near : 0u;                           // (not ok: y is exactly zero)
+    // coordinates to be decided again, by the whole warp
     const float* tab = value ? p.tv : p.tk;
     for (uint32_t who; (who = __ballot_sync(0xffffffffu, near != 0)) != 0;) {
       const int src = __ffs(who) - 1, vv = (warp & 3) * 32 + src;
       const int k = __ffs(__shfl_sync(0xffffffffu, near, src)) - 1, i = g * 32 + k;
-      double d = 0.0;
+      double d = 0.0, n = 0.0;
 #pragma unroll
-      for (int j = lane; j < D; j += 32) d = fma((double)__ldg(p.Pi + (size_t)i * D + j), tile.elem(vv, j), d);
-      const double y = warp_sum(d) / norm[vv];
+      for (int j = lane; j < D; j += 32) {
+        const double e = tile.elem(vv, j);
+        d = fma((double)__ldg(p.Pi + (size_t)i * D + j), e, d);
+        n = fma(e, e, n);
+      }
+      n = sqrt(warp_sum(n));
+      d = warp_sum(d);
+      const double y = n > 0.0 && n <= 1.7976931348623157e308 ? d / n : 0.0;
       int idx = 0;
       for (int b = 0; b < (1 << bits) - 1; ++b) idx += (double)tab[b] < y ? 1 : 0;
       if (lane == src) {
@@ -365,11 +381,33 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     if (rec >= 0) {
       uint32_t* dst = (value ? p.v_codes : p.k_codes) + (rec * G + g) * bits;
       for (int b = 0; b < bits; ++b) dst[b] = words[b];
-      if (g == 0) (value ? p.v_norms : p.k_norms)[rec] = __half_as_ushort(__double2half(n));
+    }
+    if (g == 0) {                                                // the length: whole warps
+      float f1n, f2n;
+      pow2_pair(E - 14, f1n, f2n);
+      const float n = most < 0x7F800000u ? len * f1n * f2n : __uint_as_float(most);
+      __half hn = __float2half_rn(n);
+      bool again = rec >= 0 && (far || most >= 0x7F800000u ||
+                                (ok && __half_as_ushort(__float2half_rn(n * (1.f - kBandN))) != __half_as_ushort(__float2half_rn(n * (1.f + kBandN)))));
+      for (uint32_t who; (who = __ballot_sync(0xffffffffu, again)) != 0;) {
+        const int src = __ffs(who) - 1, vv = (warp & 3) * 32 + src;
+        double m = 0.0;
+#pragma unroll
+        for (int j = lane; j < D; j += 32) {
+          const double e = tile.elem(vv, j);
+          m = fma(e, e, m);
+        }
+        m = sqrt(warp_sum(m));
+        if (lane == src) {
+          again = false;
+          hn = __double2half(m);
+        }
+      }
+      if (rec >= 0) (value ? p.v_norms : p.k_norms)[rec] = __half_as_ushort(hn);
     }
     if (!alg2) {
       tc_fence_before();
-      __syncthreads();                                           // norms and records are read
+      __syncthreads();                                           // the operands' and parts' space is free
       continue;
     }
     // ---- Pi^T c[idx] -----------------------------------------------------------------------------------------
@@ -377,19 +415,22 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     for (int b = 0; b < 4; ++b) codes[(v * G + g) * 4 + b] = words[b];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      float w[8];
+      uint32_t w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int at = 8 * c + k;
         const int idx = ((words[0] >> at) & 1) | ((words[1] >> at) & 1) << 1 | ((words[2] >> at) & 1) << 2;
-        w[k] = p.cv[idx] * kSplitScale;
+        w[k] = level[idx];
       }
       const uint32_t off = sw128_offset(v, (g * 32 + c * 8) * 2, kVec);
-      split8(w, smem + L::kOpHi + off, smem + L::kOpLo + off);
+      *(uint4*)(smem + L::kOpHi + off) = make_uint4(__byte_perm(w[0], w[1], 0x5410u), __byte_perm(w[2], w[3], 0x5410u),
+                                                    __byte_perm(w[4], w[5], 0x5410u), __byte_perm(w[6], w[7], 0x5410u));
+      *(uint4*)(smem + L::kOpLo + off) = make_uint4(__byte_perm(w[0], w[1], 0x7632u), __byte_perm(w[2], w[3], 0x7632u),
+                                                    __byte_perm(w[4], w[5], 0x7632u), __byte_perm(w[6], w[7], 0x7632u));
     }
     if (!product(L::kPiHi, true)) break;
     // ---- r = u - Pi^T c, gamma ---------------------------------------------------------------------------------
-    double gs = 0.0;
+    float gs = 0.f;
 #pragma unroll
     for (int c = 0; c < 32; c += 16) {
       uint32_t a[16], b[16];
@@ -400,7 +441,7 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
       for (int k = 0; k < 16; ++k) {
         const float e = fmaf(__uint_as_float(b[k]), kSplitScaleInv, __uint_as_float(a[k])) * kSplitScaleInv;
         x[c + k] = ok ? fmaf(x[c + k], inv, -e) : 0.f;
-        gs = fma((double)x[c + k], (double)x[c + k], gs);
+        gs = fmaf(x[c + k], x[c + k], gs);
       }
     }
 #pragma unroll
@@ -429,37 +470,43 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
         near |= (uint32_t)(fabsf(s) < kBandS * kResScale) << (c + k);
       }
     }
-    if (!ok || rec < 0) near = 0;                                // r is exactly zero
+    if (!ok) near = 0;                                           // r is exactly zero
     for (uint32_t who; (who = __ballot_sync(0xffffffffu, near != 0)) != 0;) {
       const int src = __ffs(who) - 1, vv = (warp & 3) * 32 + src;
       const int k = __ffs(__shfl_sync(0xffffffffu, near, src)) - 1, i = g * 32 + k;
       // (S r)_i = S_i u - T_i c in fp64. T is rounded to fp32: off by 2^-24 |T_i| |c| at most
-      double su = 0.0, tc = 0.0, tt = 0.0, cc = 0.0;
+      auto level_of = [&](int q) {
+        const uint32_t* w = codes + (vv * G + (q >> 5)) * 4;
+        const int at = q & 31;
+        return (double)p.cv[((w[0] >> at) & 1) | ((w[1] >> at) & 1) << 1 | ((w[2] >> at) & 1) << 2];
+      };
+      double su = 0.0, tc = 0.0, tt = 0.0, cc = 0.0, nn = 0.0;
+#pragma unroll
       for (int j = lane; j < D; j += 32) {
-        const uint32_t* w = codes + (vv * G + (j >> 5)) * 4;
-        const int at = j & 31, idx = ((w[0] >> at) & 1) | ((w[1] >> at) & 1) << 1 | ((w[2] >> at) & 1) << 2;
-        const double tij = (double)__ldg(p.T + (size_t)i * D + j), cj = (double)p.cv[idx];
-        su = fma((double)__ldg(p.S + (size_t)i * D + j), tile.elem(vv, j), su);
+        const double tij = (double)__ldg(p.T + (size_t)i * D + j), cj = level_of(j), e = tile.elem(vv, j);
+        su = fma((double)__ldg(p.S + (size_t)i * D + j), e, su);
+        nn = fma(e, e, nn);
         tc = fma(tij, cj, tc);
         tt = fma(tij, tij, tt);
         cc = fma(cj, cj, cc);
       }
-      const double un = 1.0 / norm[vv];
-      su = warp_sum(su);
-      double s = su * un - warp_sum(tc);
+      nn = sqrt(warp_sum(nn));
+      double s = warp_sum(su) / nn - warp_sum(tc);
       tt = warp_sum(tt);
       cc = warp_sum(cc);
-      if (fabs(s) <= 6e-8 * sqrt(tt * cc) + 1e-12) {             // still undecided: T_i from S and Pi themselves
-        s = 0.0;
-        for (int j = 0; j < D; ++j) {
-          double a = 0.0;
-          for (int q = lane; q < D; q += 32) {
-            const uint32_t* w = codes + (vv * G + (q >> 5)) * 4;
-            const int at = q & 31, idx = ((w[0] >> at) & 1) | ((w[1] >> at) & 1) << 1 | ((w[2] >> at) & 1) << 2;
-            a = fma((double)__ldg(p.Pi + (size_t)q * D + j), (double)p.cv[idx], a);
-          }
-          s = fma((double)__ldg(p.S + (size_t)i * D + j), tile.elem(vv, j) / norm[vv] - warp_sum(a), s);
+      if (fabs(s) <= 6e-8 * sqrt(tt * cc) + 1e-12) {             // still undecided: r itself, lane = coordinates
+        double a[G] = {};
+#pragma unroll 4
+        for (int q = 0; q < D; ++q) {
+          const double c = level_of(q);
+#pragma unroll
+          for (int j = 0; j < G; ++j) a[j] = fma((double)__ldg(p.Pi + (size_t)q * D + 32 * j + lane), c, a[j]);
         }
+        s = 0.0;
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+          s = fma((double)__ldg(p.S + (size_t)i * D + 32 * j + lane), tile.elem(vv, 32 * j + lane) / nn - a[j], s);
+        s = warp_sum(s);
       }
       if (lane == src) {
         near &= near - 1;
@@ -469,10 +516,10 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     if (rec >= 0) {
       p.v_signs[rec * G + g] = sign;
       if (g == 0) {
-        gs = 0.0;
+        gs = 0.f;
 #pragma unroll
         for (int k = 0; k < G; ++k) gs += part[k * kVec + v];
-        p.v_gammas[rec] = __half_as_ushort(__double2half(sqrt(gs)));
+        p.v_gammas[rec] = __half_as_ushort(__float2half_rn(sqrtf(gs)));
       }
     }
     tc_fence_before();
@@ -532,8 +579,8 @@ extern "C" TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t token
   p.Pi = (const float*)((const uint8_t*)rot + RL.pi32);
   p.S = (const float*)((const uint8_t*)rot + RL.s32);
   p.T = (const float*)((const uint8_t*)rot + RL.t32);
-  p.pi_hi = (const uint8_t*)rot + RL.pi_hi;
-  p.pi_lo = (const uint8_t*)rot + RL.pi_lo;
+  const size_t img[4] = {RL.pi_hi, RL.pi_lo, RL.s_hi, RL.s_lo};
+  for (int i = 0; i < 4; ++i) p.img[i] = (const uint8_t*)rot + img[i];
   p.k_codes = kv->k_codes;
   p.k_norms = kv->k_norms;
   p.v_codes = kv->v_codes;
@@ -559,5 +606,7 @@ extern "C" TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t token
     e = cudaGetLastError();
     return e == cudaSuccess ? TQ_OK : cuda_fail(e, "tq_paged_append: launch");
   };
-  return kv->d == 128 ? go(append_kernel<128>, AppendLayout<128>::kTotal, 512) : go(append_kernel<64>, AppendLayout<64>::kTotal, 256);
+  if (kv->d == 128)
+    return p.f32 ? go(append_kernel<128, true>, AppendLayout<128>::kTotal, 512) : go(append_kernel<128, false>, AppendLayout<128>::kTotal, 512);
+  return p.f32 ? go(append_kernel<64, true>, AppendLayout<64>::kTotal, 256) : go(append_kernel<64, false>, AppendLayout<64>::kTotal, 256);
 }

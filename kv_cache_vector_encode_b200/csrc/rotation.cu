@@ -34,6 +34,10 @@ RotLayout rot_layout(int d) {
   L.pit_lo = off; off += f16;
   L.st_hi = off; off += f16;
   L.st_lo = off; off += f16;
+  if (d <= 128) {
+    L.s_hi = off; off += f16;
+    L.s_lo = off; off += f16;
+  }
   L.total = off;
   return L;
 }
@@ -155,6 +159,8 @@ extern "C" TQ_API tq_status tq_rotation_prepare(int32_t d, const float* Pi, cons
                                        (__half*)(base + L.t_lo));
   split_kernel<<<blocks, 256, 0, st>>>(Pi, d, L.dp, true, (__half*)(base + L.pit_hi), (__half*)(base + L.pit_lo));
   split_kernel<<<blocks, 256, 0, st>>>(S, d, L.dp, true, (__half*)(base + L.st_hi), (__half*)(base + L.st_lo));
+  if (d <= 128)
+    split_kernel<<<blocks, 256, 0, st>>>(S, d, L.dp, false, (__half*)(base + L.s_hi), (__half*)(base + L.s_lo));
   header_kernel<<<1, 1, 0, st>>>((int*)base, d);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tq_rotation_prepare: launch");
   return TQ_OK;

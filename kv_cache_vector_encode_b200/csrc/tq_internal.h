@@ -30,10 +30,11 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 //   T_hi,  T_lo    : fp16 split of T
 //   PiT_hi, PiT_lo : fp16 split of Pi^T
 //   ST_hi,  ST_lo  : fp16 split of S^T
+//   S_hi,   S_lo   : fp16 split of S (d <= 128 only; else absent)
 struct RotLayout {
   int d, dp;
   size_t pi32, s32, t32;
-  size_t pi_hi, pi_lo, t_hi, t_lo, pit_hi, pit_lo, st_hi, st_lo;
+  size_t pi_hi, pi_lo, t_hi, t_lo, pit_hi, pit_lo, st_hi, st_lo, s_hi, s_lo;
   size_t total;
 };
 RotLayout rot_layout(int d);

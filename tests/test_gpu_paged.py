@@ -262,6 +262,9 @@ def test_append_values_at_the_edges(dev, tokens):
         x[2, 1] *= 1e-30
         x[3, 0] = 0
         x[3, 1] = 1e38
+        x[4, 0] = x[4, 0] * 1e-39                                # subnormal
+        x[4, 1] = np.where(np.arange(d) == 7, 1e-45, 0)
+        x[5, 0] = np.sign(x[5, 0]) * 3e38
     slots = rng.permutation(pages * ps)[:tokens]
     tq.tq_paged_append(kv, torch.from_numpy(k).to(dev), torch.from_numpy(v).to(dev), torch.from_numpy(slots).to(dev), rotation(d, dev)[2])
     tq.tq_sync_check()
