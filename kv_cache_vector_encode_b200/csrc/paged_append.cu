@@ -76,7 +76,7 @@ struct AppendLayout {
 template <int D>
 struct AppendTile {
   const AppendParams& p;
-  int64_t v0;                          // first vector
+  int v0;                              // first vector
   bool value;
   __device__ __forceinline__ double raw(int64_t base, int e) const {
     return p.f32 ? (double)((const float*)(value ? p.v : p.k))[base + e]
@@ -84,7 +84,7 @@ struct AppendTile {
   }
   // element e of vector v of the tile (turned), as fp64: for the coordinates that are decided again
   __device__ __forceinline__ double elem(int v, int e) const {
-    const int64_t t = (v0 + v) / p.Hkv;
+    const int t = (v0 + v) / p.Hkv;
     const int64_t base = t * (value ? p.v_stride : p.k_stride) + ((v0 + v) - t * p.Hkv) * D;
     const double x = raw(base, e);
     if (value || e >= 2 * p.half) return x;
@@ -116,35 +116,58 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint8_t* hi, uint8_t
   *(uint4*)lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Index of y: #{t < y} for the symmetric boundaries (P the positive ones), and whether y is within the band of one.
-template <int BITS>
-__device__ __forceinline__ int index_of(float y, const float (&P)[8], bool& near) {
-  const float a = fabsf(y);
-  const int m = sym_m<BITS>(a + kBandY, P);
-  near = a < kBandY || m != sym_m<BITS>(a - kBandY, P);
-  constexpr int H = 1 << (BITS - 1);
-  return y > 0.f ? H + m : H - 1 - m;
-}
-
-// Code words of a thread's 32 coordinates from the two accumulators (columns at, at + 128), y = (a + 2^-12 b) inv.
+// Code words of a thread's 32 coordinates from the two accumulators (columns at, at + 128), y = (a + 2^-12 b) inv, and
+// the mask of those within the band of a boundary. The boundaries are symmetric: with m = #{positive ones below |y|}
+// the index is H + m above zero and H - 1 - m below, so plane i is bit i of m, flipped where y is negative. A bit is
+// the sign of a difference, shifted into its word; the smallest difference tells whether any coordinate is near.
 template <int BITS>
 __device__ __forceinline__ uint32_t code_words(uint32_t at, float inv, const float (&P)[8], uint32_t (&words)[4]) {
-  uint32_t near = 0;
+  constexpr int M = (1 << (BITS - 1)) - 1;                       // positive boundaries
+  uint32_t neg = 0, w[3] = {0, 0, 0}, near = 0;
 #pragma unroll
-  for (int c = 0; c < 32; c += 16) {
+  for (int c = 16; c >= 0; c -= 16) {
     uint32_t a[16], b[16];
     tmem_ld16(at + c, a);
     tmem_ld16(at + 128 + c, b);
     tmem_ld_wait();
+    uint32_t mask = 0;
+    float nearest = INFINITY;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      bool close;
-      const int idx = index_of<BITS>(fmaf(__uint_as_float(b[k]), kSplitScaleInv, __uint_as_float(a[k])) * inv, P, close);
+    for (int k = 15; k >= 0; --k) {
+      const float y = fmaf(__uint_as_float(b[k]), kSplitScaleInv, __uint_as_float(a[k])) * inv, m = fabsf(y);
+      neg = __funnelshift_l(__float_as_uint(y), neg, 1);
+      float d[M > 0 ? M : 1], least = m;                         // negative where the boundary is below |y|
 #pragma unroll
-      for (int i = 0; i < BITS; ++i) words[i] |= (uint32_t)((idx >> i) & 1) << (c + k);
-      near |= (uint32_t)close << (c + k);
+      for (int i = 0; i < M; ++i) {
+        d[i] = P[i] - m;
+        least = fminf(least, fabsf(d[i]));
+      }
+      nearest = fminf(nearest, least);
+      a[k] = __float_as_uint(least);
+      if (BITS == 2) w[0] = __funnelshift_l(__float_as_uint(d[0]), w[0], 1);
+      if (BITS == 3) {
+        w[1] = __funnelshift_l(__float_as_uint(d[1 % (M + 1)]), w[1], 1);
+        w[0] = __funnelshift_l(__float_as_uint(d[1 % (M + 1)] < 0.f ? d[2 % (M + 1)] : d[0]), w[0], 1);
+      }
+      if (BITS == 4) {
+        const bool m2 = d[3 % (M + 1)] < 0.f;
+        const float d1 = m2 ? d[5 % (M + 1)] : d[1 % (M + 1)];
+        const bool m1 = d1 < 0.f;
+        const float lo = m1 ? d[2 % (M + 1)] : d[0], hi = m1 ? d[6 % (M + 1)] : d[4 % (M + 1)];
+        w[2] = __funnelshift_l(__float_as_uint(d[3 % (M + 1)]), w[2], 1);
+        w[1] = __funnelshift_l(__float_as_uint(d1), w[1], 1);
+        w[0] = __funnelshift_l(__float_as_uint(m2 ? hi : lo), w[0], 1);
+      }
     }
+    if (nearest < kBandY) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) mask |= (uint32_t)(__uint_as_float(a[k]) < kBandY) << k;
+    }
+    near |= mask << c;
   }
+#pragma unroll
+  for (int i = 0; i < BITS - 1; ++i) words[i] = w[i] ^ neg;
+  words[BITS - 1] = ~neg;
   return near;
 }
 
@@ -191,9 +214,9 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     for (int k = 0; k < NR; ++k) f.raw[k] = make_uint4(0, 0, 0, 0);
     if (item >= 2 * p.tiles) return;
     const bool value = item < p.tiles;
-    const int64_t n = (int64_t)(value ? item : item - p.tiles) * kVec + v, t = n / p.Hkv;
+    const int n = (value ? item : item - p.tiles) * kVec + v, t = n / p.Hkv;   // below 2^31: checked by the host
     if (t >= p.tokens) return;
-    const int h = (int)(n - t * p.Hkv);
+    const int h = n - t * p.Hkv;
     const int64_t base = t * (value ? p.v_stride : p.k_stride) + (int64_t)h * D + g * 32;
     const uint4* src = (const uint4*)((const uint8_t*)(value ? p.v : p.k) + base * (F32 ? 4 : 2));
     const int64_t slot = p.slots[t];
@@ -256,7 +279,7 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
 #pragma unroll 1
   for (int item = blockIdx.x; item < 2 * p.tiles; item += gridDim.x) {
     const bool value = item < p.tiles, alg2 = value && p.v_signs;
-    const AppendTile<D> tile{p, (int64_t)(value ? item : item - p.tiles) * kVec, value};
+    const AppendTile<D> tile{p, (value ? item : item - p.tiles) * kVec, value};
     const int64_t rec = in.rec;
     float x[32];
     uint32_t most = 0;                                           // bits of the largest magnitude
@@ -275,25 +298,58 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     }
     // ---- turn, with the partners through shared memory ---------------------------------------------------------
     if (!value && p.half) {                                      // uniform over the block
-      float* raw = (float*)(smem + L::kOpHi);                    // [coordinate][vector]
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        raw[(g * 32 + k) * kVec + v] = x[k];
-        most |= x[k] != 0.f ? 1u : 0u;
-      }
-      __syncthreads();
+      const int rot = 2 * p.half, e0 = g * 32;
       const float2* row = p.table + (int64_t)(rec < 0 ? 0 : in.pos) * p.half;
-      const int rot = 2 * p.half;
-      if (rec >= 0 && g * 32 < rot) {
+      const bool turn = rec >= 0 && e0 < rot;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int e = g * 32 + k;
-          const int pair = p.pairs ? e >> 1 : (e < p.half ? e : e - p.half);
-          const bool second = p.pairs ? e & 1 : e >= p.half;
-          if (e < rot) {
-            const float2 cs = __ldg(row + pair);
-            const float o = raw[(p.pairs ? e ^ 1 : (second ? e - p.half : e + p.half)) * kVec + v];
-            x[k] = fmaf(x[k], cs.x, second ? o * cs.y : -(o * cs.y));
+      for (int k = 0; k < 32; ++k) most |= x[k] != 0.f ? 1u : 0u;
+      const bool wide = ((uintptr_t)p.table & 15) == 0;          // rows of the table then are, for the cases that ask
+      if (p.pairs && rot % 32 == 0 && wide) {                    // both halves of a pair are here
+        if (turn) {
+          const float4* cs = (const float4*)(row + e0 / 2);      // half is a multiple of 16: rows are 16-byte aligned
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 w = __ldg(cs + k);
+            const float a0 = x[4 * k], b0 = x[4 * k + 1], a1 = x[4 * k + 2], b1 = x[4 * k + 3];
+            x[4 * k] = fmaf(a0, w.x, -(b0 * w.y));
+            x[4 * k + 1] = fmaf(b0, w.x, a0 * w.y);
+            x[4 * k + 2] = fmaf(a1, w.z, -(b1 * w.w));
+            x[4 * k + 3] = fmaf(b1, w.z, a1 * w.w);
+          }
+        }
+      } else {
+        float* raw = (float*)(smem + L::kOpHi);                  // [coordinate][vector]
+#pragma unroll
+        for (int k = 0; k < 32; ++k) raw[(e0 + k) * kVec + v] = x[k];
+        __syncthreads();
+        if (!p.pairs && p.half % 32 == 0 && wide) {                      // a group is all first or all second halves
+          if (turn) {
+            const bool second = e0 >= p.half;
+            const int other = second ? e0 - p.half : e0 + p.half;
+            const float4* cs = (const float4*)(row + (second ? e0 - p.half : e0));
+            const float sign = second ? 1.f : -1.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float4 w = __ldg(cs + k);
+              x[2 * k] = fmaf(x[2 * k], w.x, raw[(other + 2 * k) * kVec + v] * (sign * w.y));
+              x[2 * k + 1] = fmaf(x[2 * k + 1], w.z, raw[(other + 2 * k + 1) * kVec + v] * (sign * w.w));
+            }
+          }
+        } else if (turn) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 16) {                     // loads of sixteen coordinates at a time
+            float2 cs[16];
+            float o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int e = e0 + c + k, at = e < rot ? e : 0;
+              const bool second = p.pairs ? at & 1 : at >= p.half;
+              cs[k] = __ldg(row + (p.pairs ? at >> 1 : (second ? at - p.half : at)));
+              o[k] = raw[(p.pairs ? at ^ 1 : (second ? at - p.half : at + p.half)) * kVec + v] * (second ? cs[k].y : -cs[k].y);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (e0 + c + k < rot) x[c + k] = fmaf(x[c + k], cs[k].x, o[k]);
           }
         }
       }
