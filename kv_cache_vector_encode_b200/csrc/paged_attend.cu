@@ -123,13 +123,16 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 }
 
 // ---- partial results together, back to the original domain ---------------------------------------------
-// o' = sum of an item's parts, then Pi^T o'_c + alpha S^T o'_z: warp = a run of matrix rows, lane = D / 32 columns.
-constexpr int kCombThreads = 256;
+// o' = sum of an item's parts, then Pi^T o'_c + alpha S^T o'_z: warp = a run of matrix rows, lane = D / 32 columns. What a
+// step waits for is latency, so the matrices are fetched before the partial results are there, and those all at once.
+constexpr int kCombThreads = 256, kCombParts = 64;
 template <int D, bool ALG2, int RB>
 __global__ void __launch_bounds__(kCombThreads) combine_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int PD = ALG2 ? 2 * D : D, V = D / 32, W = kCombThreads / 32, J = D / W;
+  constexpr int PD = ALG2 ? 2 * D : D, V = D / 32, W = kCombThreads / 32, J = D / W, PER = RB * PD / kCombThreads;
+  static_assert(PER >= 1 && RB <= W, "one output of a row at least per thread, one warp per row");
   __shared__ float so[RB][PD];
   __shared__ __align__(16) float red[W][RB][D];
+  __shared__ float share[RB][kCombParts];                        // weights of a run of parts
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x, unit = item / p.row_blocks, rb = item - unit * p.row_blocks;
   const int b = unit / p.Hkv, hkv = unit - b * p.Hkv;
@@ -140,33 +143,53 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(const __grid_cons
     return;
   }
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
-  Vec m[J];
+  Vec m[J], ms[ALG2 ? J : 1];
 #pragma unroll
-  for (int j = 0; j < J; ++j) m[j] = __ldg((const Vec*)(p.Pi + (size_t)(warp * J + j) * D) + lane);
+  for (int j = 0; j < J; ++j) {
+    m[j] = __ldg((const Vec*)(p.Pi + (size_t)(warp * J + j) * D) + lane);
+    if (ALG2) ms[j] = __ldg((const Vec*)(p.S + (size_t)(warp * J + j) * D) + lane);
+  }
   grid_dep_wait();
   const int2 parts = p.parts[item];
-#pragma unroll 1
-  for (int e = threadIdx.x; e < RB * PD; e += kCombThreads) {
-    const int u = e / PD, i = e % PD;
-    float o = 0.f, l = 0.f, top = -INFINITY;
-    if (row0 + u < rows) {
-      for (int k = 0; k < parts.y; ++k) top = fmaxf(top, p.ml[(int64_t)(parts.x + k) * RB + u].x);
-      if (top == -INFINITY) top = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < parts.y; ++k) {
-        const int64_t at = (int64_t)(parts.x + k) * RB + u;
-        const float2 ml = p.ml[at];
-        const float f = ex2_approx(ml.x - top);
-        l = fmaf(f, ml.y, l);
-        o = fmaf(f, p.po[at * PD + i], o);
+  float top = -INFINITY, l = 0.f, o[PER] = {};
+  // warp u: the parts' largest reference and the sum of row u, lane = part
+  if (warp < RB && row0 + warp < rows) {
+    for (int k = lane; k < parts.y; k += 32) top = fmaxf(top, p.ml[(int64_t)(parts.x + k) * RB + warp].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (top == -INFINITY) top = 0.f;
+    for (int k = lane; k < parts.y; k += 32) {
+      const float2 ml = p.ml[(int64_t)(parts.x + k) * RB + warp];
+      l = fmaf(ex2_approx(ml.x - top), ml.y, l);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;                    // NaN stays NaN
+  for (int k0 = 0; k0 < parts.y; k0 += kCombParts) {
+    const int n = min(kCombParts, parts.y - k0);
+    if (warp < RB)
+      for (int k = lane; k < n; k += 32)
+        share[warp][k] = row0 + warp < rows ? ex2_approx(p.ml[(int64_t)(parts.x + k0 + k) * RB + warp].x - top) * inv : 0.f;
+    __syncthreads();
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const int at = threadIdx.x + e * kCombThreads, u = at / PD;
+        if (row0 + u < rows) o[e] = fmaf(share[u][k], p.po[(int64_t)(parts.x + k0 + k) * (RB * PD) + at], o[e]);
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;                  // NaN stays NaN
-    so[u][i] = (ALG2 && i >= D ? p.alpha : 1.f) * o * inv;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int at = threadIdx.x + e * kCombThreads, u = at / PD, i = at % PD;
+    so[u][i] = (ALG2 && i >= D ? p.alpha : 1.f) * o[e];
   }
   __syncthreads();
   float acc[RB][V] = {};
-  auto rows_times = [&](const Vec (&mat)[J], int at) {
+  auto rows_times = [&](const Vec* mat, int at) {
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -177,11 +200,7 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(const __grid_cons
       }
   };
   rows_times(m, 0);
-  if (ALG2) {
-#pragma unroll
-    for (int j = 0; j < J; ++j) m[j] = __ldg((const Vec*)(p.S + (size_t)(warp * J + j) * D) + lane);
-    rows_times(m, D);
-  }
+  if (ALG2) rows_times(ms, D);
 #pragma unroll
   for (int u = 0; u < RB; ++u)
 #pragma unroll

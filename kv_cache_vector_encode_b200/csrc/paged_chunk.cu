@@ -453,7 +453,7 @@ __device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t phase, uint32_
 }
 
 // S_FULL, P_FULL: [group][half]
-enum CBars { Q_FULL = 0, KV_FULL = 2, KV_EMPTY = 10, S_FULL = 18, P_FULL = 22, PV_DONE = 26, CNBARS = 28 };
+enum CBars { Q_FULL = 0, KV_FULL = 2, KV_EMPTY = 10, S_FULL = 18, P_FULL = 22, PV_DONE = 26, O_FULL = 28, CNBARS = 30 };
 
 // the n lowest bits of 32
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int u = 0; u < 2; ++u) {
       mbar_init(&bar[Q_FULL + u], 4);
       mbar_init(&bar[PV_DONE + u], 1);
+      mbar_init(&bar[O_FULL + u], 1);
       for (int k = 0; k < 2; ++k) {
         mbar_init(&bar[S_FULL + 2 * u + k], 1);
         mbar_init(&bar[P_FULL + 2 * u + k], 4);
@@ -662,6 +663,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int ks = 0; ks < kTile / 32; ++ks)
             mma_ts(to, ts + 64 * half + 8 * ks, b + 2 * ks, idesc_f16_f32(128, D), i > 0 || ks > 0);
           mma_commit(&bar[PV_DONE + u]);
+          if (i + 1 == 2 * n) mma_commit(&bar[O_FULL + u]);
           if (half) mma_commit(&bar[KV_EMPTY + kv % NS]);
         }
         __syncwarp();
@@ -763,6 +765,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ref = nr;
         sum *= g;
         if (i > 0) {
+          // step i - 1's product; that of step i - 2 is done, since the scores of step i came after it
           ok = wait_soon(&bar[PV_DONE + u], (i - 1) & 1, p.err, kDevTimeoutMma, abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -801,7 +804,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       sum = fmaf((l2[0].x + l2[0].y) + (l2[1].x + l2[1].y), cur.z, sum);
     }
     // ---- out = O / sum ------------------------------------------------------------------------------------
-    if (n > 0 && ok) ok = wait_soon(&bar[PV_DONE + u], 1, p.err, kDevTimeoutMma, abort_flag);   // of step 2 n - 1
+    // (a barrier of its own: PV_DONE shows the parity of a phase, which may be that of the product before last)
+    if (n > 0 && ok) ok = wait_soon(&bar[O_FULL + u], 0, p.err, kDevTimeoutMma, abort_flag);
     if (ok) {
       tc_fence_after();
       const float inv = sum == 0.f ? 0.f : __int_as_float((127 - kBits) << 23) / sum;

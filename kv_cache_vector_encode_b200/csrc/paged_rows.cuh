@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
     }
     __syncthreads();
   }
-  grid_dep_wait();                                               // the queries come from the kernel before
   grid_dep_launch();
+  bool waited = false;
 
   uint32_t ktab[4], vtab[4];
 #pragma unroll
@@ -214,46 +214,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
         const int t0 = (int)(lo + 16 * (pos - base)), t1 = (int)min(hi, lo + 16 * (stop - base));
         const int nblk = (int)(stop - pos);
         const int item = (b * p.Hkv + hkv) * p.row_blocks + rb;
-        if (pos == base && threadIdx.x == 0) {
-          const int last = (int)(((base + nb) * start.ctas - 1) / start.total);   // the CTA of the item's last block
-          p.parts[item] = make_int2(blockIdx.x + item, last - (int)blockIdx.x + 1);
-        }
+        const bool opens = pos == base;                          // the item's first part
         pos = stop;
 
-        // this lane's query rows (c and c + 4 of the block)
-        int qpos[NB];
-        // ref is the reference (from: the same, 0 in the empty state), elim a power of two >= every value norm seen
-        // and room what its inverse times kRowRoom is
-        float fac[NB], slope[NB], ref[NB], from[NB], sum[NB], wsum[NB], zsum[NB], elim[NB], room[NB];
-        int qsum[NB];
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          const int row = row0 + c + 4 * u;
-          const bool on = row < rows;
-          const int j = on ? row / p.g : 0, h = hkv * p.g + (on ? row - j * p.g : 0);
-          const int64_t at = (int64_t)item * RB + c + 4 * u;
-          qpos[u] = on ? (int)first + j : -1;
-          fac[u] = on ? p.key_fac * p.qs[at].x : 0.f;
-          qsum[u] = on && KB == 4 ? __float_as_int(p.qs[at].y) : 0;
-          slope[u] = on && p.slopes ? p.slopes[h] * kLog2e : 0.f;
-          ref[u] = -INFINITY;
-          sum[u] = wsum[u] = zsum[u] = 0.f;
-          from[u] = elim[u] = 0.f;
-          room[u] = 1.f;
-        }
-        // query limbs: column 2 h + limb of block u is head row h + 4 u
-        uint32_t qf[NB][D / 16];
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          const int row = (r >> 1) + 4 * u;
-          const bool on = row0 + row < rows;
-          const uint4* src = (const uint4*)(p.qr + (((int64_t)item * RB + (on ? row : 0)) * 2 + (r & 1)) * D + c * (D / 4));
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const uint4 v = on ? src[i] : make_uint4(0, 0, 0, 0);
-            qf[u][4 * i] = v.x, qf[u][4 * i + 1] = v.y, qf[u][4 * i + 2] = v.z, qf[u][4 * i + 3] = v.w;
-          }
-        }
         // outputs: columns c and c + 4 of a product. With four rows the sign plane's go where the rows c + 4 would be
         constexpr bool SHARE = ALG2 && NB == 1;
         float oc[MB][4], oz[ALG2 && !SHARE ? MB : 1][4];
@@ -309,6 +272,48 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           const int page = page_next;
           page_next = page_of(warp + (k + 1) * kRowWarps);
           issue(warp + k * kRowWarps, page, k);
+        }
+        if (!waited) {
+          grid_dep_wait();                                       // the queries come from the kernel before
+          waited = true;
+        }
+        if (opens && threadIdx.x == 0) {
+          const int last = (int)(((base + nb) * start.ctas - 1) / start.total);   // the CTA of the item's last block
+          p.parts[item] = make_int2(blockIdx.x + item, last - (int)blockIdx.x + 1);
+        }
+        // this lane's query rows (c and c + 4 of the block)
+        int qpos[NB];
+        // ref is the reference (from: the same, 0 in the empty state), elim a power of two >= every value norm seen
+        // and room what its inverse times kRowRoom is
+        float fac[NB], slope[NB], ref[NB], from[NB], sum[NB], wsum[NB], zsum[NB], elim[NB], room[NB];
+        int qsum[NB];
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          const int row = row0 + c + 4 * u;
+          const bool on = row < rows;
+          const int j = on ? row / p.g : 0, h = hkv * p.g + (on ? row - j * p.g : 0);
+          const int64_t at = (int64_t)item * RB + c + 4 * u;
+          qpos[u] = on ? (int)first + j : -1;
+          fac[u] = on ? p.key_fac * p.qs[at].x : 0.f;
+          qsum[u] = on && KB == 4 ? __float_as_int(p.qs[at].y) : 0;
+          slope[u] = on && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+          ref[u] = -INFINITY;
+          sum[u] = wsum[u] = zsum[u] = 0.f;
+          from[u] = elim[u] = 0.f;
+          room[u] = 1.f;
+        }
+        // query limbs: column 2 h + limb of block u is head row h + 4 u
+        uint32_t qf[NB][D / 16];
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          const int row = (r >> 1) + 4 * u;
+          const bool on = row0 + row < rows;
+          const uint4* src = (const uint4*)(p.qr + (((int64_t)item * RB + (on ? row : 0)) * 2 + (r & 1)) * D + c * (D / 4));
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            const uint4 v = on ? src[i] : make_uint4(0, 0, 0, 0);
+            qf[u][4 * i] = v.x, qf[u][4 * i + 1] = v.y, qf[u][4 * i + 2] = v.z, qf[u][4 * i + 3] = v.w;
+          }
         }
         // tokens [open_lo, open_hi) are seen by every row (and those before the prefix)
         const int open_lo = p.window > 0 ? (int)first + jhi - p.window + 1 : 0, open_hi = min((int)first + jlo + 1, t1);

@@ -569,6 +569,20 @@ def test_attend_opens_units_in_groups(dev):
     tq.tq_sync_check()
 
 
+@pytest.mark.parametrize("case", [8, 12, 14, 7])
+def test_attend_many_times(dev, case):
+    """The same call 40 times over, bit for bit: hand-offs between warps that a single call seldom shows."""
+    lens, q_lens, Hq, Hkv, d, kb, vb, alg, ps, opt = CASES[case]
+    rng = np.random.default_rng(case)
+    pool = Paged(dev, lens, Hkv, d, kb, vb, alg, ps, seed=case)
+    q = queries(rng, sum(q_lens), Hq, d, dev)
+    opt = {k: v for k, v in opt.items() if k not in ("prefix", "slopes")}
+    outs = [pool.call(q, q_lens, **opt) for _ in range(40)]
+    tq.tq_sync_check()
+    pool.check(outs[0], q, q_lens, **opt)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
 def test_attend_dirty_workspace_and_single_rows(dev):
     """A workspace of NaN bytes, one token, one query of one head."""
     pool = Paged(dev, [1, 3], 1, 64, 1, 2, 2, 16, seed=1)
