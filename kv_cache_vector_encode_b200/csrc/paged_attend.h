@@ -138,23 +138,17 @@ __device__ __forceinline__ uint32_t nibbles(const uint32_t* w, int s) {
     x |= (s >= b ? w[b] >> (s - b) : w[b] << (b - s)) & (0x11111111u << b);
   return x;
 }
-// Level indices as nibbles: nibble n of the result = index of coordinate s + 4 n (n = 0..3 from a shift of 16 h
-// + s). For 16 levels the nibble is the magnitude's index and `neg` has bit 0 of nibble n set where the
-// level is negative.
+// Of 16 levels: the index planes into those of the magnitudes, and the bits where the level is negative.
 template <int BITS>
-__device__ __forceinline__ uint32_t pick(const uint32_t* w, int shift, uint32_t& neg) {
-  uint32_t x = 0;
+__device__ __forceinline__ uint32_t magnitudes(uint32_t (&w)[BITS]) {
   if constexpr (BITS == 4) {
-    neg = (~w[3] >> shift) & 0x11111111u;
     const uint32_t f = ~w[3];
 #pragma unroll
-    for (int b = 0; b < 3; ++b) x |= (((w[b] ^ f) >> shift) & 0x11111111u) << b;
+    for (int i = 0; i < 3; ++i) w[i] ^= f;
+    return f;
   } else {
-#pragma unroll
-    for (int b = 0; b < BITS; ++b) x |= ((w[b] >> shift) & 0x11111111u) << b;
-    neg = 0;
+    return 0u;
   }
-  return x;
 }
 // Four levels from the low four nibbles of `sel`: (0, 1) and (2, 3) as fp16 pairs.
 template <int BITS>

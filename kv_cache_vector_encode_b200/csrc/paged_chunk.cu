@@ -265,10 +265,11 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
         sg_lo = (h & 255u) * 0x0101u;
         sg_hi = ((h >> 8) ^ 0x80u) | ((h >> 8) << 8);
       }
+      const uint32_t kf = magnitudes<KB>(kw), vf = magnitudes<VB>(vw);
 #pragma unroll
       for (int s4 = 0; s4 < 4; ++s4) {
-        uint32_t nk, nv;
-        const uint32_t xk = pick<KB>(kw, s4, nk), xv = pick<VB>(vw, s4, nv);
+        const uint32_t xk = nibbles<KB>(kw, s4), xv = nibbles<VB>(vw, s4);
+        const uint32_t nk = KB == 4 ? (kf >> s4) & 0x11111111u : 0u, nv = VB == 4 ? (vf >> s4) & 0x11111111u : 0u;
         uint32_t a[4], b[4];
         look_up<KB>(xk, nk, ktab, a[0], a[1]);
         look_up<KB>(xk >> 16, nk >> 16, ktab, a[2], a[3]);

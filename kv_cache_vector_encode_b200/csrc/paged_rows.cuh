@@ -344,12 +344,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
               wb[i] = st[L::kKey + ((r + 8) * G + grp) * KB + i];
               if (D == 64 && (c & 1)) wa[i] >>= 16, wb[i] >>= 16;
             }
-            uint32_t fa = 0, fb = 0;
-            if constexpr (KB == 4) {                             // magnitudes; f has a bit where the level is negative
-              fa = ~wa[3], fb = ~wb[3];
-#pragma unroll
-              for (int i = 0; i < 3; ++i) wa[i] ^= fa, wb[i] ^= fb;
-            }
+            const uint32_t fa = magnitudes<KB>(wa), fb = magnitudes<KB>(wb);
             // four levels' bytes from the low four nibbles of sel
             auto bytes = [&](uint32_t sel, uint32_t flip, uint32_t& hi8, uint32_t& lo8) {
               hi8 = __byte_perm(ktab[2], ktab[3], sel);
@@ -517,21 +512,33 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           if constexpr (VB == 1) {
             plane(L::kVal, oc, pc[0], pc[1]);
           } else {
+            // lane r: 16 coordinates of group r / 2 (d = 128), or 8 of group r / 4, of each of its four tokens
+            const int grp = D == 128 ? r >> 1 : r >> 2, shift = D == 128 ? 2 * (r & 1) : r & 3;
+            uint32_t w[4][VB], flip[4];
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-              uint32_t e[4][2];
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+              for (int i = 0; i < VB; ++i) w[k][i] = st[L::kVal + (tk[k] * G + grp) * VB + i] >> shift;
+              flip[k] = magnitudes<VB>(w[k]);
+            }
+#pragma unroll
+            for (int s4 = 0; s4 < D / 64; ++s4) {
+              uint32_t x[4], neg[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                uint32_t w[VB], neg;
-#pragma unroll
-                for (int i = 0; i < VB; ++i) w[i] = st[L::kVal + (tk[k] * G + g) * VB + i];
-                const uint32_t sel = pick<VB>(w, (r & 3) + 16 * (r >> 2), neg);
-                look_up<VB>(sel, neg, vtab, e[k][0], e[k][1]);
+                x[k] = nibbles<VB>(w[k], s4);
+                neg[k] = VB == 4 ? (flip[k] >> s4) & 0x11111111u : 0u;
               }
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                mma_f16(oc[2 * g + h], __byte_perm(e[0][h], e[1][h], 0x5410u), __byte_perm(e[0][h], e[1][h], 0x7632u),
-                        __byte_perm(e[2][h], e[3][h], 0x5410u), __byte_perm(e[2][h], e[3][h], 0x7632u), pc[0], pc[1]);
+              for (int q = 0; q < 2; ++q) {
+                uint32_t t[4][2];                                // [token][pair]: levels of coordinates 4 q + 2 pair, + 1
+#pragma unroll
+                for (int k = 0; k < 4; ++k) look_up<VB>(x[k] >> (16 * q), neg[k] >> (16 * q), vtab, t[k][0], t[k][1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  mma_f16(oc[4 * s4 + 2 * q + h], __byte_perm(t[0][h], t[1][h], 0x5410u), __byte_perm(t[0][h], t[1][h], 0x7632u),
+                          __byte_perm(t[2][h], t[3][h], 0x5410u), __byte_perm(t[2][h], t[3][h], 0x7632u), pc[0], pc[1]);
+              }
             }
           }
           if constexpr (SHARE) plane(L::kSign, oc, pz[0], pz[1]);
@@ -571,7 +578,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
                   const int i = D == 128 ? m + 8 * h : r + 8 * h;
                   dst[at + (D == 128 ? 16 * r : 16 * m) + i] = (i == 15 ? -v : fmaf(2.f * v, inv_bit(i), -total)) * unit;
                 } else {
-                  dst[at + 32 * (m >> 1) + (r & 3) + 16 * (r >> 2) + 4 * (2 * (m & 1) + h)] = v * unit;
+                  const int e = 2 * m + h;                       // as the look-up yields them
+                  dst[at + (D == 128 ? 32 * (r >> 1) + 2 * (r & 1) + (e >> 3) + 4 * (e & 7) : 32 * (r >> 2) + (r & 3) + 4 * e)] = v * unit;
                 }
               }
           };
