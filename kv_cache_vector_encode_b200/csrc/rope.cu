@@ -153,11 +153,12 @@ tq_status launch_rope(RopeParams& p, int d, bool half_layout, bool in_place, cud
   p.turn_runs = p.half / np;
   p.rest0 = rot;
   p.runs = p.turn_runs + (in_place ? 0 : (d - rot) / nv);
-  // enough units to fill the device (eight blocks of 256 per SM), but no more than needed: each reads
-  // its part of the table once
-  const int64_t want = (int64_t)sm_count() * 8 * 256;
-  int64_t splits = want / (p.tokens * p.runs) + 1;
-  p.splits = (int)(splits < p.heads ? splits : p.heads);
+  // as many units as run at a time (eight blocks of 256 per SM), not more: each reads its part of the table once, and
+  // a second wave of a few blocks costs as much as the first
+  const int64_t want = (int64_t)sm_count() * 8 * 256, fit = want / (p.tokens * p.runs);
+  const int splits = (int)(fit < 1 ? 1 : fit < p.heads ? fit : p.heads);
+  const int each = (p.heads + splits - 1) / splits;              // heads of a unit
+  p.splits = (p.heads + each - 1) / each;
   p.units = p.tokens * p.splits * p.runs;
   const int64_t grid = (p.units + 255) / 256;
   if (grid > 2147483647LL) return fail(TQ_ERR_UNSUPPORTED, "tq_rope: too many elements for one call");
