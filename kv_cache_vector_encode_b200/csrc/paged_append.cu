@@ -409,7 +409,11 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
              : bits == 3 ? code_words<3>(mine, inv, P, words)
                          : code_words<4>(mine, inv, P, words);
     }
-    near = far ? ~0u : ok ? near : 0u;                           // (not ok: y is exactly zero)
+    near = far ? ~0u : ok ? near : 0u;
+    if (!ok) {                                                   // y is exactly zero: index 2^(bits-1) - 1
+#pragma unroll
+      for (int b = 0; b < 4; ++b) words[b] = b < bits - 1 ? ~0u : 0u;
+    }
     // coordinates to be decided again, by the whole warp
     const float* tab = value ? p.tv : p.tk;
     for (uint32_t who; (who = __ballot_sync(0xffffffffu, near != 0)) != 0;) {
