@@ -393,7 +393,7 @@ TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t tokens, const vo
                                  const int32_t* positions, const float* table, int64_t n_pos, int32_t rot_dim,
                                  int32_t layout, const void* rot, void* stream);
 
-/* Workspace bytes of tq_paged_attend for these sizes (0 for invalid sizes). */
+/* Workspace bytes of tq_paged_attend for these sizes on the current device (0 for invalid sizes, or no work). */
 TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, int32_t Hq, int64_t total_q,
                                               int32_t max_q_len, int64_t max_kv_len);
 
@@ -402,7 +402,7 @@ TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, 
  * t % page_size; its Qn = q_start[b+1] - q_start[b] newest tokens are the queries q_start[b] .. of q, query j
  * at position pos = kv_len[b] - Qn + j:
  *   x_t   = scale <q[j][h], k_hat_t>                        (k_hat, v_hat: the decoded records)
- *   x_t   = softcap tanh(x_t / softcap)                     (softcap > 0)
+ *   x_t   = softcap tanh(x_t / softcap)                     (softcap >= 1e-30; 0: no cap)
  *   x_t  += slopes[h] (t - pos)                             (slopes given: a bias by distance)
  *   seen:   t < kv_len[b] and ((t <= pos and (window = 0 or t > pos - window)) or t < prefix_len[b])
  *   out[j][h] = sum over seen t of softmax_t(x) v_hat_t;    0 where nothing is seen
@@ -415,12 +415,17 @@ TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, 
  *   slopes      [Hq] fp32 or NULL
  *   scale       0 (or any value that is not > 0) selects 1/sqrt(d)
  *   out         [total_q][Hq][d] TQ_BF16, contiguous
- * Lengths or page numbers outside their ranges are reported by tq_sync_check (TQ_ERR_DEVICE_INPUT); such
- * tokens are taken as not seen. Scores, softmax and sums in fp32; queries, levels and softmax weights enter
- * the tensor cores as fp16. Hq a multiple of Hkv, Hq / Hkv <= 128, B up to 65535. B and total_q may be 0.
- * ws: caller device workspace of at least tq_paged_attend_workspace_bytes(...) bytes; calls that may
- * overlap on the GPU (two streams, two captured graphs) need one each. Errors: INVALID_ARG, UNSUPPORTED,
- * WORKSPACE, CUDA. */
+ * Lengths or page numbers outside their ranges are reported by tq_sync_check (TQ_ERR_DEVICE_INPUT): a bad page's
+ * tokens, and those past max_kv_len or max_pages, are taken as not seen; a sequence with a bad q_start has no
+ * queries, and its outputs are left as they were. A record with a norm that is not finite makes the rows that see
+ * it not finite, and no others.
+ * Softmax and sums in fp32. A sequence with few query rows per KV head (Qn Hq / Hkv up to 48) meets the codes
+ * themselves: its queries and the key levels enter the tensor cores as 16-bit integers, value levels and softmax
+ * weights as fp16. A longer chunk's visible tokens are decoded once into fp16 tiles in the workspace, by groups of
+ * (sequence, KV head) pairs that share 1 GiB of it (one pair at least: 4 d bytes per token).
+ * Hq a multiple of Hkv, Hq / Hkv <= 128, B Hkv up to 65535, max_q_len Hq / Hkv up to 2^24 - 256. B and total_q may be
+ * 0. ws: caller device workspace of at least tq_paged_attend_workspace_bytes(...) bytes; calls that may overlap on
+ * the GPU (two streams, two captured graphs) need one each. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, int32_t Hq, int64_t total_q, int32_t max_q_len,
                                  int64_t max_kv_len, const void* q, int64_t q_token_stride, int32_t q_dtype,
                                  const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,

@@ -328,7 +328,8 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   if (work && (!q || !q_start || !kv_len || !page_table || !rot || !out)) return fail(TQ_ERR_INVALID_ARG, f + ": NULL pointer");
   if (q_dtype != TQ_BF16) return fail(TQ_ERR_UNSUPPORTED, f + ": q must be TQ_BF16");
   if (max_pages < 0 || window < 0) return fail(TQ_ERR_INVALID_ARG, f + ": negative max_pages or window");
-  if (!(softcap >= 0.0f) || std::isinf(softcap)) return fail(TQ_ERR_INVALID_ARG, f + ": softcap must be finite and >= 0");
+  if (!(softcap == 0.0f || softcap >= 1e-30f) || std::isinf(softcap))
+    return fail(TQ_ERR_INVALID_ARG, f + ": softcap must be finite, and 0 (none) or at least 1e-30");
   if (std::isinf(scale)) return fail(TQ_ERR_INVALID_ARG, f + ": scale must be finite");
   if (q_token_stride < (int64_t)Hq * kv->d) return fail(TQ_ERR_INVALID_ARG, f + ": q_token_stride < Hq d");
   if (!aligned16(q) || !aligned16(out) || !aligned16(rot) || !aligned16(ws) || q_token_stride % 8)

@@ -20,7 +20,6 @@ enum DeviceError : uint32_t {
   kDevTimeoutMma = 2,      // a tcgen05.commit never arrived
   kDevTimeoutSync = 3,     // a producer/consumer hand-off never arrived
   kDevTmemAlloc = 4,
-  kDevBadInput = 16,       // an index in device data (position, slot, page, length) out of its range
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -44,7 +44,10 @@ constexpr float kSplitScaleInv = 1.0f / 4096.0f;
 
 bool valid_dim(int d);       // multiple of 32 in [32, 4096]
 
-// Device address of the library's error word (kernels record bounded-wait timeouts there).
+// Code of an index in device data (position, slot, page, length) out of its range, next to sm100.cuh's DeviceError.
+constexpr uint32_t kDevBadInput = 16;
+
+// Device address of the library's error word (kernels record bounded-wait timeouts and bad indices there).
 uint32_t* device_error_word();
 
 // Number of SMs of the current device.

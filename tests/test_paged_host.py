@@ -121,7 +121,7 @@ def test_attend_refusals(L):
     assert call(Hq=12) == uns and call(Hq=8 * 129) == uns and call(B=65535) == uns and call(mkv=1 << 31) == uns
     assert call(total=1 << 29, mq=2) == uns and call(mq=1 << 30) == uns
     assert call(q=None) == bad and call(lens=None) == bad and call(R=None) == bad and call(dt=tq.TQ_F32) == uns
-    assert call(mp=-1) == bad and call(window=-1) == bad and call(cap=-1.0) == bad and call(cap=float("nan")) == bad
+    assert call(mp=-1) == bad and call(window=-1) == bad and call(cap=-1.0) == bad and call(cap=1e-38) == bad and call(cap=float("nan")) == bad
     assert call(scale=float("inf")) == bad and call(qs=32 * 128 - 8) == bad and call(qs=32 * 128 + 4) == bad
     assert call(q=P + 2) == bad and call(lens=P + 2) == bad and call(slopes=P + 1) == bad and call(out=P + 4) == bad
     need = L.tq_paged_attend_workspace_bytes(ctypes.byref(kv), 2, 32, 4, 2, 100)
