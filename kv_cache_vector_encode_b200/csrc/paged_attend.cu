@@ -37,15 +37,20 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
   __shared__ float red[RB][D / 32];
   __shared__ int isum[RB][D / 32];
   grid_dep_launch();
+  constexpr int PI = D * D / 4 / kPrepThreads;                   // the longest way first
+  float4 pi[PI];
+#pragma unroll
+  for (int k = 0; k < PI; ++k) pi[k] = __ldg((const float4*)p.Pi + threadIdx.x + k * kPrepThreads);
   const int item = blockIdx.x, unit = item / p.row_blocks, rb = item - unit * p.row_blocks;
   const int b = unit / p.Hkv, hkv = unit - b * p.Hkv;
   if (threadIdx.x == 0) p.parts[item] = make_int2(0, 0);
   const PagedSeq s = paged_seq(p, b);
   const int row0 = rb * RB, rows = s.qn * p.g;
   if (row0 >= rows || rows > p.chunk_rows) return;
-  for (int e = threadIdx.x; e < D * D / 4; e += kPrepThreads) {
-    const float4 v = __ldg((const float4*)p.Pi + e);
-    *(float4*)&mat[(e / (D / 4)) * (D + 4) + (e % (D / 4)) * 4] = v;
+#pragma unroll
+  for (int k = 0; k < PI; ++k) {
+    const int e = threadIdx.x + k * kPrepThreads;
+    *(float4*)&mat[(e / (D / 4)) * (D + 4) + (e % (D / 4)) * 4] = pi[k];
   }
   for (int e = threadIdx.x; e < RB * D; e += kPrepThreads) {
     const int row = row0 + e / D, j = row / p.g;
@@ -125,10 +130,10 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 // ---- partial results together, back to the original domain ---------------------------------------------
 // o' = sum of an item's parts, then Pi^T o'_c + alpha S^T o'_z: warp = a run of matrix rows, lane = D / 32 columns. What a
 // step waits for is latency, so the matrices are fetched before the partial results are there, and those all at once.
-constexpr int kCombThreads = 256, kCombParts = 64;
+constexpr int kCombThreads = 256, kCombParts = 64;   // threads; parts of a pass where there are many
 template <int D, bool ALG2, int RB>
 __global__ void __launch_bounds__(kCombThreads) combine_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int PD = ALG2 ? 2 * D : D, V = D / 32, W = kCombThreads / 32, J = D / W, PER = RB * PD / kCombThreads;
+  constexpr int PD = ALG2 ? 2 * D : D, V = D / 32, W = kCombThreads / 32, J = D / W, PER = RB * PD / kCombThreads, FEW = PER <= 4 ? 8 : 4;   // outputs of a thread; parts fetched at once
   static_assert(PER >= 1 && RB <= W, "one output of a row at least per thread, one warp per row");
   __shared__ float so[RB][PD];
   __shared__ __align__(16) float red[W][RB][D];
@@ -151,36 +156,60 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(const __grid_cons
   }
   grid_dep_wait();
   const int2 parts = p.parts[item];
+  const bool mine = warp < RB && row0 + warp < rows;             // warp u: the shares of row u's parts, lane = part
+  const float2* ml = p.ml + (int64_t)parts.x * RB + warp;
+  const float* po = p.po + (int64_t)parts.x * (RB * PD) + threadIdx.x;
   float top = -INFINITY, l = 0.f, o[PER] = {};
-  // warp u: the parts' largest reference and the sum of row u, lane = part
-  if (warp < RB && row0 + warp < rows) {
-    for (int k = lane; k < parts.y; k += 32) top = fmaxf(top, p.ml[(int64_t)(parts.x + k) * RB + warp].x);
+  if (parts.y <= FEW) {                                     // all at once
+    const float2 x = mine && lane < parts.y ? ml[lane * RB] : make_float2(-INFINITY, 0.f);
+    float v[FEW][PER];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (top == -INFINITY) top = 0.f;
-    for (int k = lane; k < parts.y; k += 32) {
-      const float2 ml = p.ml[(int64_t)(parts.x + k) * RB + warp];
-      l = fmaf(ex2_approx(ml.x - top), ml.y, l);
+    for (int k = 0; k < FEW; ++k)
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        v[k][e] = k < parts.y && row0 + (int)(threadIdx.x + e * kCombThreads) / PD < rows ? po[(int64_t)k * (RB * PD) + e * kCombThreads] : 0.f;
+    if (warp < RB) {
+      top = x.x;
+#pragma unroll
+      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      const float f = ex2_approx(x.x - (top == -INFINITY ? 0.f : top));
+      l = f * x.y;
+#pragma unroll
+      for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+      if (lane < FEW) share[warp][lane] = lane < parts.y ? f * (l == 0.f ? 0.f : 1.f / l) : 0.f;   // NaN stays NaN
     }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;                    // NaN stays NaN
-  for (int k0 = 0; k0 < parts.y; k0 += kCombParts) {
-    const int n = min(kCombParts, parts.y - k0);
-    if (warp < RB)
-      for (int k = lane; k < n; k += 32)
-        share[warp][k] = row0 + warp < rows ? ex2_approx(p.ml[(int64_t)(parts.x + k0 + k) * RB + warp].x - top) * inv : 0.f;
     __syncthreads();
+#pragma unroll
+    for (int k = 0; k < FEW; ++k)
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (k < parts.y) o[e] = fmaf(share[(threadIdx.x + e * kCombThreads) / PD][k], v[k][e], o[e]);
+  } else {
+    if (mine) {
+      for (int k = lane; k < parts.y; k += 32) top = fmaxf(top, ml[k * RB].x);
+#pragma unroll
+      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      if (top == -INFINITY) top = 0.f;
+      for (int k = lane; k < parts.y; k += 32) l = fmaf(ex2_approx(ml[k * RB].x - top), ml[k * RB].y, l);
+#pragma unroll
+      for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int k0 = 0; k0 < parts.y; k0 += kCombParts) {
+      const int n = min(kCombParts, parts.y - k0);
+      if (warp < RB)
+        for (int k = lane; k < n; k += 32) share[warp][k] = mine ? ex2_approx(ml[(k0 + k) * RB].x - top) * inv : 0.f;
+      __syncthreads();
 #pragma unroll 8
-    for (int k = 0; k < n; ++k) {
+      for (int k = 0; k < n; ++k) {
 #pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const int at = threadIdx.x + e * kCombThreads, u = at / PD;
-        if (row0 + u < rows) o[e] = fmaf(share[u][k], p.po[(int64_t)(parts.x + k0 + k) * (RB * PD) + at], o[e]);
+        for (int e = 0; e < PER; ++e) {
+          const int u = (threadIdx.x + e * kCombThreads) / PD;
+          if (row0 + u < rows) o[e] = fmaf(share[u][k], po[(int64_t)(k0 + k) * (RB * PD) + e * kCombThreads], o[e]);
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
