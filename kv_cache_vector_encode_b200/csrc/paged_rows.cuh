@@ -24,6 +24,9 @@
 // CTA (two CTAs per SM): ragged batches cost no waiting, and a CTA's start and end are paid once per range, not
 // once per split of every sequence. A CTA's part of an item is a partial result in slot (CTA + item), which no
 // other part can share; the first part of an item records (first slot, parts) for the combine kernel.
+// Short batches are latency: a part costs some 4 us before and after its blocks, whose time is 0.6 us for eight (one per
+// warp). Where it lengthens a range by less than that, items are therefore cut into parts of their own, none of which
+// shares a CTA (4 sequences of 1000 tokens: 22.5 -> 15 us).
 // Inside a part the eight warps take the blocks in turn, each with a softmax state and a cp.async ring of its own
 // (no barrier in the loop). Lane = 4 r + c holds tokens r and r + 8 for the rows c and c + 4.
 // The softmax reference of a row moves only when a score passes it by more than 8 (log2 domain), so that the
@@ -40,6 +43,7 @@ namespace tq {
 
 constexpr int kRowWarps = 8;
 constexpr int kRowStages = 4;
+constexpr int kRowSlack = 48;     // blocks by which a range may grow to hold a part of one item alone
 constexpr float kRowLazy = 8.0f;  // how far (log2) a score may pass the reference before it moves
 constexpr float kRowRoom = 64.0f; // weights are below 2^8 and enter fp16 times this (times a residual norm, below 2)
 
@@ -123,12 +127,13 @@ __device__ __forceinline__ int row_blocks_of(const PagedAttendParams& p, const P
   return hi > lo ? (int)((hi - lo + 15) >> 4) : 0;
 }
 
-// Where CTA `cta` of `ctas` starts: the item that holds block cta * total / ctas.
+// Where a CTA starts. Its range counts blocks of all items, or (unit > 0) parts of all items, of `unit` blocks at most.
 struct RowStart {
-  int64_t pos, end, total;      // this CTA's blocks; all blocks
-  int b, ctas;                  // sequence of the first block, CTAs that take part
-  int64_t base;                 // first block of that sequence
+  int64_t pos, end, total;      // this CTA's range; blocks or parts of all items
+  int64_t base;                 // first block or part of sequence b
+  int b, ctas, unit;            // sequence that the range starts in; CTAs that take part
 };
+__device__ __forceinline__ int row_parts(int blocks, int unit) { return unit > 0 ? (blocks + unit - 1) / unit : blocks; }
 
 template <int D, int KB, int VB, bool ALG2, int NB>
 __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_constant__ PagedAttendParams p) {
@@ -141,46 +146,61 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
 
   // ---- this CTA's range: every CTA adds up the batch's blocks, each thread a run of sequences -------------------
   {
-    auto blocks_of = [&](int b) {
+    auto count = [&](int b, int unit) {
       const PagedSeq s = paged_seq_quiet(p, b);
       const int64_t prefix = p.prefix ? min((int64_t)p.prefix[b], s.kv) : 0;
       int64_t lo, hi, n = 0;
-      for (int rb = 0; rb < p.row_blocks; ++rb) n += row_blocks_of(p, s, prefix, rb, lo, hi);
+      for (int rb = 0; rb < p.row_blocks; ++rb) n += row_parts(row_blocks_of(p, s, prefix, rb, lo, hi), unit);
       return n * p.Hkv;
     };
     const int per = (p.B + NT - 1) / NT, b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += blocks_of(b);
-    int64_t before = mine;
+    int64_t mine, before, total;
+    auto add_up = [&](int unit) {
+      mine = 0;
+      for (int b = b0; b < b1; ++b) mine += count(b, unit);
+      before = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += v;
-    }
-    if (lane == 31) sums[warp] = before;
-    __syncthreads();
-    int64_t total = 0;
-    before -= mine;
-    for (int w = 0; w < kRowWarps; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
-    }
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      if (lane == 31) sums[warp] = before;
+      __syncthreads();
+      total = 0;
+      before -= mine;
+      for (int w = 0; w < kRowWarps; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+      }
+    };
+    add_up(0);
     // at least a block per warp: fewer CTAs where there is less
-    const int ctas = (int)min((int64_t)gridDim.x, (total + kRowWarps - 1) / kRowWarps);
+    int ctas = (int)min((int64_t)gridDim.x, (total + kRowWarps - 1) / kRowWarps), unit = 0;
+    const int64_t items = (int64_t)p.B * p.Hkv * p.row_blocks;
+    if (items < (int64_t)gridDim.x) {                            // parts of `whole` blocks fit, whatever the items' lengths
+      const int64_t whole = max((int64_t)kRowWarps, (total + gridDim.x - items - 1) / (gridDim.x - items));
+      if (whole <= total / gridDim.x + kRowSlack) {
+        __syncthreads();                                         // the sums have been read
+        unit = (int)whole;
+        add_up(unit);
+        ctas = (int)total;
+      }
+    }
     if ((int)blockIdx.x >= ctas) {                               // uniform
       grid_dep_wait();                                           // the next kernel may rely on the one before this
       return;
     }
-    const int64_t pos = (int64_t)blockIdx.x * total / ctas, end = (int64_t)(blockIdx.x + 1) * total / ctas;
+    const int64_t pos = unit ? blockIdx.x : (int64_t)blockIdx.x * total / ctas;
+    const int64_t end = unit ? blockIdx.x + 1 : (int64_t)(blockIdx.x + 1) * total / ctas;
     if (pos >= before && pos < before + mine) {
       int b = b0;
       int64_t base = before;
       for (; b + 1 < b1; ++b) {
-        const int64_t n = blocks_of(b);
+        const int64_t n = count(b, unit);
         if (pos < base + n) break;
         base += n;
       }
-      start = RowStart{pos, end, total, b, ctas, base};
+      start = RowStart{pos, end, total, base, b, ctas, unit};
     }
     __syncthreads();
   }
@@ -201,18 +221,29 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
     const int64_t prefix = p.prefix ? min((int64_t)p.prefix[b], sq.kv) : 0;
     const int rows = sq.qn * p.g;
     // items in the order of their numbers, so that (CTA + item) grows with every part
-    for (int hkv = 0; hkv < p.Hkv && pos < start.end; ++hkv) {
-      int nb;
-      for (int rb = 0; rb < p.row_blocks && pos < start.end; ++rb, base += nb) {
+    int hkv = 0;
+    {                                                            // KV heads that lie before the range at once
+      int64_t lo, hi, head = 0;
+      for (int rb = 0; rb < p.row_blocks; ++rb) head += row_parts(row_blocks_of(p, sq, prefix, rb, lo, hi), start.unit);
+      if (head == 0) continue;
+      hkv = (int)min((int64_t)p.Hkv, (pos - base) / head);
+      base += hkv * head;
+    }
+    for (; hkv < p.Hkv && pos < start.end; ++hkv) {
+      int np;
+      for (int rb = 0; rb < p.row_blocks && pos < start.end; ++rb, base += np) {
         int64_t lo, hi;
-        nb = row_blocks_of(p, sq, prefix, rb, lo, hi);
-        if (pos >= base + nb) continue;                          // done by CTAs before, or empty
+        const int nb = row_blocks_of(p, sq, prefix, rb, lo, hi);
+        np = row_parts(nb, start.unit);
+        if (pos >= base + np) continue;                          // done by CTAs before, or empty
         const int row0 = rb * RB;
         const int jlo = row0 / p.g, jhi = min(rows - 1, row0 + RB - 1) / p.g;
         // ---- one part: blocks [pos, stop) of item (b, hkv, rb) ------------------------------------------------
-        const int64_t stop = min(base + nb, start.end);
-        const int t0 = (int)(lo + 16 * (pos - base)), t1 = (int)min(hi, lo + 16 * (stop - base));
-        const int nblk = (int)(stop - pos);
+        const int64_t stop = min(base + np, start.end);
+        const int blk_lo = start.unit ? (int)((pos - base) * nb / np) : (int)(pos - base);
+        const int blk_hi = start.unit ? (int)((stop - base) * nb / np) : (int)(stop - base);
+        const int t0 = (int)lo + 16 * blk_lo, t1 = (int)min(hi, lo + 16 * (int64_t)blk_hi);
+        const int nblk = blk_hi - blk_lo;
         const int item = (b * p.Hkv + hkv) * p.row_blocks + rb;
         const bool opens = pos == base;                          // the item's first part
         pos = stop;
@@ -278,8 +309,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           waited = true;
         }
         if (opens && threadIdx.x == 0) {
-          const int last = (int)(((base + nb) * start.ctas - 1) / start.total);   // the CTA of the item's last block
-          p.parts[item] = make_int2(blockIdx.x + item, last - (int)blockIdx.x + 1);
+          // up to the CTA of the item's last block
+          const int n = start.unit ? np : (int)(((base + np) * start.ctas - 1) / start.total) - (int)blockIdx.x + 1;
+          p.parts[item] = make_int2(blockIdx.x + item, n);
         }
         // this lane's query rows (c and c + 4 of the block)
         int qpos[NB];
