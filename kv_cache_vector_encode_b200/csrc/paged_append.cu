@@ -171,10 +171,11 @@ __device__ __forceinline__ uint32_t code_words(uint32_t at, float inv, const flo
   return near;
 }
 
-// What a thread fetches of an item: its vector's record number and 32 coordinates, as they come.
+// What a thread fetches of an item: its vector's slot and position and its 32 coordinates, as they come (nothing waits
+// for them until the item's turn).
 struct AppendFetch {
-  int64_t rec;                 // -1: nothing to write
-  int pos;
+  int64_t slot;                // negative: nothing to write
+  int pos, h;                  // position, head
   uint4 raw[8];
 };
 
@@ -208,8 +209,8 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     level[tid] = (uint32_t)__half_as_ushort(h) | (uint32_t)__half_as_ushort(__float2half_rn((c - __half2float(h)) * kSplitScale)) << 16;
   }
   auto fetch = [&](int item, AppendFetch& f) {
-    f.rec = -1;
-    f.pos = 0;
+    f.slot = -1;
+    f.pos = f.h = 0;
 #pragma unroll
     for (int k = 0; k < NR; ++k) f.raw[k] = make_uint4(0, 0, 0, 0);
     if (item >= 2 * p.tiles) return;
@@ -219,14 +220,11 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     const int h = n - t * p.Hkv;
     const int64_t base = t * (value ? p.v_stride : p.k_stride) + (int64_t)h * D + g * 32;
     const uint4* src = (const uint4*)((const uint8_t*)(value ? p.v : p.k) + base * (F32 ? 4 : 2));
-    const int64_t slot = p.slots[t];
-    f.pos = p.half ? p.positions[t] : 0;
+    f.h = h;
+    f.slot = p.slots[t];
+    if (p.half) f.pos = p.positions[t];
 #pragma unroll
     for (int k = 0; k < NR; ++k) f.raw[k] = __ldg(src + k);
-    if (slot >= p.slots_total || (slot >= 0 && p.half && (f.pos < 0 || f.pos >= p.n_pos)))
-      atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
-    else if (slot >= 0)
-      f.rec = (((slot >> p.page_shift) * p.Hkv + h) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
   };
   AppendFetch in;
   fetch(blockIdx.x, in);
@@ -280,7 +278,11 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
   for (int item = blockIdx.x; item < 2 * p.tiles; item += gridDim.x) {
     const bool value = item < p.tiles, alg2 = value && p.v_signs;
     const AppendTile<D> tile{p, (value ? item : item - p.tiles) * kVec, value};
-    const int64_t rec = in.rec;
+    int64_t rec = -1;                                            // record number
+    if (in.slot >= p.slots_total || (in.slot >= 0 && p.half && (in.pos < 0 || in.pos >= p.n_pos)))
+      atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+    else if (in.slot >= 0)
+      rec = (((in.slot >> p.page_shift) * p.Hkv + in.h) << p.page_shift) + (in.slot & ((1 << p.page_shift) - 1));
     float x[32];
     uint32_t most = 0;                                           // bits of the largest magnitude
 #pragma unroll

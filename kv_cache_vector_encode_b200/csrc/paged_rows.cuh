@@ -115,6 +115,11 @@ struct RowStage {   // 32-bit words of a 16-token stage
   static constexpr size_t smem() { return ring() > merge() ? ring() : merge(); }
 };
 
+// Quotient of non-negative numbers that seldom need their 64 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // 16-token blocks of row block rb of a sequence (none for the chunk kernels' sequences).
 __device__ __forceinline__ int row_blocks_of(const PagedAttendParams& p, const PagedSeq& s, int64_t prefix, int rb, int64_t& lo,
                                              int64_t& hi) {
@@ -122,7 +127,8 @@ __device__ __forceinline__ int row_blocks_of(const PagedAttendParams& p, const P
   lo = hi = 0;
   if (row0 >= rows || rows > p.chunk_rows) return 0;
   const int64_t first = s.kv - s.qn;
-  paged_range(p, s, first + row0 / p.g, first + min(rows - 1, row0 + p.rows_per_item - 1) / p.g, prefix, lo, hi);
+  const int j0 = row0 == 0 ? 0 : row0 / p.g, j1 = row0 + p.rows_per_item >= rows ? s.qn - 1 : (row0 + p.rows_per_item - 1) / p.g;
+  paged_range(p, s, first + j0, first + j1, prefix, lo, hi);
   lo &= ~15LL;
   return hi > lo ? (int)((hi - lo + 15) >> 4) : 0;
 }
@@ -178,8 +184,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
     int ctas = (int)min((int64_t)gridDim.x, (total + kRowWarps - 1) / kRowWarps), unit = 0;
     const int64_t items = (int64_t)p.B * p.Hkv * p.row_blocks;
     if (items < (int64_t)gridDim.x) {                            // parts of `whole` blocks fit, whatever the items' lengths
-      const int64_t whole = max((int64_t)kRowWarps, (total + gridDim.x - items - 1) / (gridDim.x - items));
-      if (whole <= total / gridDim.x + kRowSlack) {
+      const int64_t whole = max((int64_t)kRowWarps, quotient(total + gridDim.x - items - 1, gridDim.x - items));
+      if (whole <= quotient(total, gridDim.x) + kRowSlack) {
         __syncthreads();                                         // the sums have been read
         unit = (int)whole;
         add_up(unit);
@@ -190,8 +196,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
       grid_dep_wait();                                           // the next kernel may rely on the one before this
       return;
     }
-    const int64_t pos = unit ? blockIdx.x : (int64_t)blockIdx.x * total / ctas;
-    const int64_t end = unit ? blockIdx.x + 1 : (int64_t)(blockIdx.x + 1) * total / ctas;
+    const int64_t pos = unit ? blockIdx.x : quotient(blockIdx.x * total, ctas);
+    const int64_t end = unit ? blockIdx.x + 1 : quotient((blockIdx.x + 1) * total, ctas);
     if (pos >= before && pos < before + mine) {
       int b = b0;
       int64_t base = before;
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
       int64_t lo, hi, head = 0;
       for (int rb = 0; rb < p.row_blocks; ++rb) head += row_parts(row_blocks_of(p, sq, prefix, rb, lo, hi), start.unit);
       if (head == 0) continue;
-      hkv = (int)min((int64_t)p.Hkv, (pos - base) / head);
+      hkv = (int)min((int64_t)p.Hkv, quotient(pos - base, head));
       base += hkv * head;
     }
     for (; hkv < p.Hkv && pos < start.end; ++hkv) {
@@ -237,11 +243,11 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
         np = row_parts(nb, start.unit);
         if (pos >= base + np) continue;                          // done by CTAs before, or empty
         const int row0 = rb * RB;
-        const int jlo = row0 / p.g, jhi = min(rows - 1, row0 + RB - 1) / p.g;
+        const int jlo = row0 == 0 ? 0 : row0 / p.g, jhi = row0 + RB >= rows ? sq.qn - 1 : (row0 + RB - 1) / p.g;
         // ---- one part: blocks [pos, stop) of item (b, hkv, rb) ------------------------------------------------
         const int64_t stop = min(base + np, start.end);
-        const int blk_lo = start.unit ? (int)((pos - base) * nb / np) : (int)(pos - base);
-        const int blk_hi = start.unit ? (int)((stop - base) * nb / np) : (int)(stop - base);
+        const int blk_lo = start.unit ? (int)quotient((pos - base) * nb, np) : (int)(pos - base);
+        const int blk_hi = start.unit ? (int)quotient((stop - base) * nb, np) : (int)(stop - base);
         const int t0 = (int)lo + 16 * blk_lo, t1 = (int)min(hi, lo + 16 * (int64_t)blk_hi);
         const int nblk = blk_hi - blk_lo;
         const int item = (b * p.Hkv + hkv) * p.row_blocks + rb;
