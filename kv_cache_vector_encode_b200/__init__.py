@@ -12,6 +12,8 @@ Names follow the C ABI. Tensors:
   signs    [n, d/32] int32
   norms    [n] float16,  gammas [n] float16
   rot      uint8 buffer of tq_rotation_bytes(d) bytes (prepared by tq_rotation_prepare)
+  table    [n_pos, rot_dim/2, 2] float32 (cos, sin) of tq_rope_table
+  PagedKV  the packed cache in pages: the arrays above with leading axes [pages, Hkv, page_size]
 """
 from __future__ import annotations
 

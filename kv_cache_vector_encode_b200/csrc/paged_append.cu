@@ -10,7 +10,10 @@
 // lengths), which with fp32 accumulation gives y and r to about 2^-19 at worst. That decides all but a few
 // coordinates as fp64 would. The others are known, since they lie within a band around a boundary that is wider
 // than the error, and are decided again by the whole warp with fp64 sums: about one in 10^4.
-// (All in fp64 on the SIMT cores, the first form of this kernel, took 1279 us for 8192 tokens of 8 heads.)
+//
+// Measured: 8192 tokens of 8 heads of 128 (K 3 bits, V 3 bits by Algorithm 2) 111 us, where all in fp64 on the SIMT cores
+// took 1279; 64 tokens 16.4 us. A tile of values takes 24 thousand cycles, of keys 12 thousand: phases that wait for
+// one another (2000 to 3000 each for the three products, 5000 for the indices), tensor pipe 12 %, issue 32 %.
 //
 // Layout: a CTA takes tiles of 128 vectors (keys or values of consecutive heads and tokens), thread = (vector, group of
 // 32 coordinates), so that a thread packs a group's code words by itself. Products have the vectors as M (TMEM

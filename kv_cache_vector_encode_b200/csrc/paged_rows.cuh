@@ -26,12 +26,16 @@
 // other part can share; the first part of an item records (first slot, parts) for the combine kernel.
 // Short batches are latency: a part costs some 4 us before and after its blocks, whose time is 0.6 us for eight (one per
 // warp). Where it lengthens a range by less than that, items are therefore cut into parts of their own, none of which
-// shares a CTA (4 sequences of 1000 tokens: 22.5 -> 15 us).
+// shares a CTA (4 sequences of 1000 tokens: 20.5 -> 16.4 us).
 // Inside a part the eight warps take the blocks in turn, each with a softmax state and a cp.async ring of its own
 // (no barrier in the loop). Lane = 4 r + c holds tokens r and r + 8 for the rows c and c + 4.
 // The softmax reference of a row moves only when a score passes it by more than 8 (log2 domain), so that the
 // accumulators are rarely rescaled; weights stay below 2^8. The value norms enter the weights, relative to the
 // largest norm seen so far (a power of two, kept with the reference), so that fp16 holds them.
+//
+// Measured: one step of 16 sequences of up to 32768 tokens (32 query heads over 8, K 3 bits, V 2) 154 us with prep and
+// combine, 1.8 TB/s of packed records; 450 warp instructions per 16 tokens, integer pipe 59 %, tensor pipe 24 %. Two
+// CTAs of eight warps per SM: three at 80 registers gain nothing (177 against 172 us).
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
