@@ -120,6 +120,16 @@ struct OpenLayout {
                             kTotal = kBar + 64 + 1024;
 };
 constexpr int kOpenThreads = 512;
+constexpr int kOpenUnits = 256;       // units whose ranges a CTA keeps (those beyond are worked out for every tile)
+struct OpenUnit {
+  int b, hkv, t0, tiles, lo, hi;      // t0: first token of the first of `tiles` tiles; visible tokens [lo, hi)
+};
+__device__ __forceinline__ OpenUnit open_unit(const PagedAttendParams& p, const ChunkParams& c, int u) {
+  Unit x;
+  if (!find_unit(p, c, u, x) || x.hi <= x.lo) return OpenUnit{0, 0, 0, 0, 0, 0};
+  const int t0 = (int)x.lo & ~(kTile - 1);
+  return OpenUnit{x.b, x.hkv, t0, ((int)x.hi - t0 + kTile - 1) / kTile, (int)x.lo, (int)x.hi};
+}
 
 template <int D, int KB, int VB, bool ALG2>
 __global__ void __launch_bounds__(kOpenThreads, 1)
@@ -163,7 +173,30 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
   uint32_t kw[KB], vw[VB], sw = 0;
   uint16_t kn = 0, vn = 0, vg = 0;
   bool present = false;
-  auto fetch = [&](int item) {
+  // A tile's page numbers are fetched two tiles ahead and its records one ahead, so that no turn waits for both.
+  __shared__ OpenUnit units[kOpenUnits];
+  for (int u = tid; u < min(c.units, kOpenUnits); u += kOpenThreads) units[u] = open_unit(p, c, u);
+  __syncthreads();
+  const int items = c.units * c.tiles;
+  int next = items, next_t = 0;                                  // the tile after the one in hand; this thread's token of it
+  bool next_want = false, next_lo = false;                       // the token is in range; it is seen by someone
+  int next_page = 0, next_hkv = 0;
+  auto locate = [&](int item) {                                  // the first tile from `item` on (in steps of the grid)
+    next_want = false;
+    for (; item < items; item += gridDim.x) {
+      const int u = item / c.tiles, k = item - u * c.tiles;
+      const OpenUnit x = u < kOpenUnits ? units[u] : open_unit(p, c, u);
+      if (k >= x.tiles) continue;
+      next_t = x.t0 + k * kTile + tok;
+      next_want = unpacker && next_t < x.hi;
+      next_lo = next_t >= x.lo;
+      next_hkv = x.hkv;
+      if (next_want) next_page = p.table[(int64_t)x.b * p.max_pages + (next_t >> p.page_shift)];
+      break;
+    }
+    next = item;
+  };
+  auto take = [&]() {
     present = false;
     kn = vn = vg = 0;
     sw = 0;
@@ -171,47 +204,35 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
     for (int i = 0; i < KB; ++i) kw[i] = 0;
 #pragma unroll
     for (int i = 0; i < VB; ++i) vw[i] = 0;
-    const int u = item / c.tiles;
-    Unit x;
-    if (u >= c.units || !find_unit(p, c, u, x)) return false;
-    const int64_t t0 = (x.lo & ~(int64_t)(kTile - 1)) + (int64_t)(item - u * c.tiles) * kTile;
-    if (t0 >= x.hi) return false;
-    if (unpacker) {
-      const int64_t t = t0 + tok;
-      if (t < x.hi) {
-        const int64_t page = p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)];
-        if (page >= 0 && page < p.num_pages) {
-          const int64_t rec = ((page * p.Hkv + x.hkv) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-          present = true;
+    if (!next_want) return;
+    if (next_page >= 0 && next_page < p.num_pages) {
+      const int64_t rec = (((int64_t)next_page * p.Hkv + next_hkv) << p.page_shift) + (next_t & ((1 << p.page_shift) - 1));
+      present = true;
 #pragma unroll
-          for (int i = 0; i < KB; ++i) kw[i] = __ldg(p.k_codes + (rec * G + grp) * KB + i);
+      for (int i = 0; i < KB; ++i) kw[i] = __ldg(p.k_codes + (rec * G + grp) * KB + i);
 #pragma unroll
-          for (int i = 0; i < VB; ++i) vw[i] = __ldg(p.v_codes + (rec * G + grp) * VB + i);
-          kn = __ldg(p.k_norms + rec);
-          vn = __ldg(p.v_norms + rec);
-          if (ALG2) {
-            sw = __ldg(p.v_signs + rec * G + grp);
-            vg = __ldg(p.v_gammas + rec);
-          }
-        } else if (t >= x.lo) {
-          atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
-        }
+      for (int i = 0; i < VB; ++i) vw[i] = __ldg(p.v_codes + (rec * G + grp) * VB + i);
+      kn = __ldg(p.k_norms + rec);
+      vn = __ldg(p.v_norms + rec);
+      if (ALG2) {
+        sw = __ldg(p.v_signs + rec * G + grp);
+        vg = __ldg(p.v_gammas + rec);
       }
+    } else if (next_lo) {
+      atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
     }
-    return true;
   };
 
-  const int items = c.units * c.tiles;
-  int item = blockIdx.x;
-  bool live = item < items && fetch(item);
+  locate(blockIdx.x);
+  int item = next;
+  if (item < items) {
+    take();
+    locate(item + gridDim.x);
+  }
   uint32_t phase = 0;
   bool loaded = false;
+#pragma unroll 1
   while (item < items) {
-    if (!live) {                                                 // uniform over the block
-      item += gridDim.x;
-      live = item < items && fetch(item);
-      continue;
-    }
     // ---- norms: factors of the tokens, exponents of the tile -------------------------------------------
     const float fk = __half2float(__ushort_as_half(kn)), fv = __half2float(__ushort_as_half(vn));
     const float fg = ALG2 ? __half2float(__ushort_as_half(vg)) : 0.f;
@@ -319,8 +340,11 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
     }
     __syncwarp();
     const int done = item;
-    item += gridDim.x;
-    live = item < items && fetch(item);
+    item = next;
+    if (item < items) {
+      take();
+      locate(item + gridDim.x);
+    }
     if (!__syncthreads_and(mbar_wait(&bar[1], phase, p.err, kDevTimeoutMma, abort_flag))) break;
     phase ^= 1;
     tc_fence_after();
