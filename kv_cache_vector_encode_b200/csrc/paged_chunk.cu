@@ -115,11 +115,12 @@ __device__ __forceinline__ bool find_unit(const PagedAttendParams& p, const Chun
 // ---- open -----------------------------------------------------------------------------------------------
 template <int D, bool ALG2>
 struct OpenLayout {
-  static constexpr uint32_t kImg = 128 * D * 2, kMat = 0, kSgn = kImg, kK = kSgn + (ALG2 ? kImg : 0), kV = kK + kImg,
-                            kS = kV + kImg, kInfo = kS + (ALG2 ? kImg : 0), kBar = kInfo + 2 * 128 * 4 + 128,
+  static constexpr uint32_t kImg = 128 * D * 2, kMat = 0, kSgn = kImg, kTiles = kSgn + (ALG2 ? kImg : 0),
+                            kS = kTiles + 3 * kImg, kInfo = kS + (ALG2 ? kImg : 0), kBar = kInfo + 2 * 128 * 4,
                             kTotal = kBar + 64 + 1024;
 };
 constexpr int kOpenThreads = 512;
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 constexpr int kOpenUnits = 256;       // units whose ranges a CTA keeps (those beyond are worked out for every tile)
 struct OpenUnit {
   int b, hkv, t0, tiles, lo, hi;      // t0: first token of the first of `tiles` tiles; visible tokens [lo, hi)
@@ -139,7 +140,6 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float* info = (float*)(smem + L::kInfo);                       // [key factor, value factor][128]
-  int* top = (int*)(info + 2 * 128);                             // [16 warps][key, value] exponents
   uint64_t* bar = (uint64_t*)(smem + L::kBar);                   // matrices loaded, products done
   uint32_t* tmem_slot = (uint32_t*)(bar + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
     take();
     locate(item + gridDim.x);
   }
-  uint32_t phase = 0;
+  uint32_t phase = 0, turn = 0;
   bool loaded = false;
 #pragma unroll 1
   while (item < items) {
@@ -239,20 +239,18 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
     const bool fine = fabsf(fk) < INFINITY && fabsf(fv) < INFINITY && fabsf(fg) < INFINITY;
     const float reach = fabsf(fv) * fmaxf(1.f, fabsf(fg));
     __shared__ uint32_t words[2][4];
+    __shared__ int top[2];                                       // largest exponent fields: keys, values
     {
       // exponent fields (of positive floats these order like the values); a token's G threads agree
-      int ek = fine ? (__float_as_int(fabsf(fk)) >> 23) : 0, ev = fine ? (__float_as_int(reach) >> 23) : 0;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        ek = max(ek, __shfl_xor_sync(0xffffffffu, ek, o));
-        ev = max(ev, __shfl_xor_sync(0xffffffffu, ev, o));
-      }
+      const int ek = __reduce_max_sync(0xffffffffu, fine ? (__float_as_int(fabsf(fk)) >> 23) : 0);
+      const int ev = __reduce_max_sync(0xffffffffu, fine ? (__float_as_int(reach) >> 23) : 0);
       if (tid < 8) words[tid >> 2][tid & 3] = 0;
-      if (tid == 0) bulk_wait_read0();                           // the images' last copy has left shared memory
+      if (tid < 2) top[tid] = 0;
+      if (tid == 0) bulk_wait_read1();                           // of the last tile's copies only the values' may still run
       __syncthreads();
       if (lane == 0 && unpacker) {
-        top[2 * warp] = ek;
-        top[2 * warp + 1] = ev;
+        atomicMax(&top[0], ek);
+        atomicMax(&top[1], ev);
       }
       if (unpacker && grp == 0) {
         if (present) atomicOr(&words[0][tok >> 5], 1u << (tok & 31));
@@ -260,30 +258,27 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
       }
     }
     __syncthreads();
-    int ek = 0, ev = 0;
-    for (int w = 0; w < kTile * G / 32; ++w) {
-      ek = max(ek, top[2 * w]);
-      ev = max(ev, top[2 * w + 1]);
-    }
     // norms times 2^-(e - 127 + 1) are below 1 (an empty tile: any exponent will do)
-    ek = ek == 0 ? 0 : ek - 126;
-    ev = ev == 0 ? 0 : ev - 126;
+    const int ek = top[0] == 0 ? 0 : top[0] - 126, ev = top[1] == 0 ? 0 : top[1] - 126;
+    auto pow2 = [](int e) { return __int_as_float((127 + e) << 23); };   // |e| up to 60 here
     if (unpacker && grp == 0) {
       const bool use = present && fine;
-      info[tok] = use ? ldexpf(fk, kBits - ek) * p.k_inv_unit : 0.f;
-      info[128 + tok] = use ? ldexpf(fv, kBits - ev) * p.v_inv_unit : 0.f;
+      info[tok] = use ? fk * pow2(kBits - ek) * p.k_inv_unit : 0.f;
+      info[128 + tok] = use ? fv * pow2(kBits - ev) * p.v_inv_unit : 0.f;
     }
-    if (tid == 0) {
+    if (tid >= kOpenThreads - 8) {                               // the head, by eight threads of the last warp
       TileHead* h = c.heads + item;
-      const bool all = (words[0][0] & words[0][1] & words[0][2] & words[0][3]) == 0xffffffffu;
-      const bool odd = (words[1][0] | words[1][1] | words[1][2] | words[1][3]) != 0;
-      h->k_unit = ldexpf(1.f, ek - kBits);
-      h->v_exp = (float)ev;
-      h->v_unit = ldexpf(1.f, -ev);
-      h->flags = (all ? 0u : 1u) | (odd ? 2u : 0u);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h->present[i] = words[0][i], h->strange[i] = words[1][i];
+      const int k = tid - (kOpenThreads - 8);
+      (k < 4 ? h->present : h->strange)[k & 3] = words[k >> 2][k & 3];
+      if (k == 0) {
+        const bool all = (words[0][0] & words[0][1] & words[0][2] & words[0][3]) == 0xffffffffu;
+        const bool odd = (words[1][0] | words[1][1] | words[1][2] | words[1][3]) != 0;
+        *(float4*)h = make_float4(pow2(ek - kBits), (float)ev, pow2(-ev), __uint_as_float((all ? 0u : 1u) | (odd ? 2u : 0u)));
+      }
     }
+    // keys and values take two of three tiles in turn, so that the copies out of one turn run on into the next
+    const uint32_t key_at = L::kTiles + (2 * turn % 3) * L::kImg, val_at = L::kTiles + ((2 * turn + 1) % 3) * L::kImg;
+    ++turn;
     // ---- unpack into operands ---------------------------------------------------------------------------
     if (unpacker) {
       uint32_t sg_lo = 0, sg_hi = 0;
@@ -303,8 +298,8 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
         look_up<VB>(xv, nv, vtab, b[0], b[1]);
         look_up<VB>(xv >> 16, nv >> 16, vtab, b[2], b[3]);
         const uint32_t off = sw128_offset(tok, (grp * 32 + s4 * 8) * 2, 128);
-        *(uint4*)(smem + L::kK + off) = make_uint4(a[0], a[1], a[2], a[3]);
-        *(uint4*)(smem + L::kV + off) = make_uint4(b[0], b[1], b[2], b[3]);
+        *(uint4*)(smem + key_at + off) = make_uint4(a[0], a[1], a[2], a[3]);
+        *(uint4*)(smem + val_at + off) = make_uint4(b[0], b[1], b[2], b[3]);
         if (ALG2) {
           const uint32_t z = (sw >> s4) & 0x11111111u;
           uint32_t o[4];
@@ -327,8 +322,8 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
     }
     tc_fence_after();
     if (warp == 0 && elect_one_sync()) {
-      const uint32_t m = smem_u32(smem + L::kMat), sg = smem_u32(smem + L::kSgn), k = smem_u32(smem + L::kK),
-                     v = smem_u32(smem + L::kV), s = smem_u32(smem + L::kS);
+      const uint32_t m = smem_u32(smem + L::kMat), sg = smem_u32(smem + L::kSgn), k = smem_u32(smem + key_at),
+                     v = smem_u32(smem + val_at), s = smem_u32(smem + L::kS);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
@@ -368,7 +363,7 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          *(uint4*)(smem + L::kK + sw128_offset(row, (part * W + c0 + 8 * i) * 2, 128)) =
+          *(uint4*)(smem + key_at + sw128_offset(row, (part * W + c0 + 8 * i) * 2, 128)) =
               make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
       }
     }
@@ -390,7 +385,7 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          *(uint4*)(smem + L::kV + sw128_offset(row, (part * 32 + c0 + 8 * i) * 2, D)) =
+          *(uint4*)(smem + val_at + sw128_offset(row, (part * 32 + c0 + 8 * i) * 2, D)) =
               make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
       }
     }
@@ -400,8 +395,9 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
     tc_fence_after();
     if (tid == 0) {
       uint8_t* dst = c.images + (size_t)done * 2 * L::kImg;
-      bulk_s2g(dst, smem + L::kK, L::kImg);
-      bulk_s2g(dst + L::kImg, smem + L::kV, L::kImg);
+      bulk_s2g(dst, smem + key_at, L::kImg);
+      bulk_commit();
+      bulk_s2g(dst + L::kImg, smem + val_at, L::kImg);
       bulk_commit();
     }
   }
