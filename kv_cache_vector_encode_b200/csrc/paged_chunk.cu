@@ -140,13 +140,12 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float* info = (float*)(smem + L::kInfo);                       // [key factor, value factor][128]
-  uint64_t* bar = (uint64_t*)(smem + L::kBar);                   // matrices loaded, products done
-  uint32_t* tmem_slot = (uint32_t*)(bar + 2);
+  uint64_t* bar = (uint64_t*)(smem + L::kBar);                   // matrices loaded; products of the keys, of the values done
+  uint32_t* tmem_slot = (uint32_t*)(bar + 3);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(&bar[0], 1);
-    mbar_init(&bar[1], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -279,26 +278,52 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
     // keys and values take two of three tiles in turn, so that the copies out of one turn run on into the next
     const uint32_t key_at = L::kTiles + (2 * turn % 3) * L::kImg, val_at = L::kTiles + ((2 * turn + 1) % 3) * L::kImg;
     ++turn;
-    // ---- unpack into operands ---------------------------------------------------------------------------
+    // ---- unpack into operands: the keys, whose product then runs while the values follow -------------------
     if (unpacker) {
+      const uint32_t kf = magnitudes<KB>(kw);
+#pragma unroll
+      for (int s4 = 0; s4 < 4; ++s4) {
+        const uint32_t xk = nibbles<KB>(kw, s4), nk = KB == 4 ? (kf >> s4) & 0x11111111u : 0u;
+        uint32_t a[4];
+        look_up<KB>(xk, nk, ktab, a[0], a[1]);
+        look_up<KB>(xk >> 16, nk >> 16, ktab, a[2], a[3]);
+        *(uint4*)(smem + key_at + sw128_offset(tok, (grp * 32 + s4 * 8) * 2, 128)) = make_uint4(a[0], a[1], a[2], a[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (!loaded) {
+      if (!__syncthreads_and(mbar_wait(&bar[0], 0, p.err, kDevTimeoutLoad, abort_flag))) break;
+      loaded = true;
+    }
+    tc_fence_after();
+    const uint32_t m = smem_u32(smem + L::kMat), sg = smem_u32(smem + L::kSgn);
+    if (warp == 0 && elect_one_sync()) {
+      const uint32_t k = smem_u32(smem + key_at);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
+        mma_f16_ss(tk, desc_kmajor_sw128(k + at), desc_kmajor_sw128(m + at), idesc_f16_f32(128, D), ks > 0);
+      }
+      mma_commit(&bar[1]);
+    }
+    __syncwarp();
+    if (unpacker) {
+      const uint32_t vf = magnitudes<VB>(vw);
       uint32_t sg_lo = 0, sg_hi = 0;
       if (ALG2) {   // alpha gamma in units of the levels, with either sign, as byte tables (z = 0: negative)
         const uint32_t h = __half_as_ushort(__float2half_rn(present && fine ? p.sign_unit * fg : 0.f));
         sg_lo = (h & 255u) * 0x0101u;
         sg_hi = ((h >> 8) ^ 0x80u) | ((h >> 8) << 8);
       }
-      const uint32_t kf = magnitudes<KB>(kw), vf = magnitudes<VB>(vw);
 #pragma unroll
       for (int s4 = 0; s4 < 4; ++s4) {
-        const uint32_t xk = nibbles<KB>(kw, s4), xv = nibbles<VB>(vw, s4);
-        const uint32_t nk = KB == 4 ? (kf >> s4) & 0x11111111u : 0u, nv = VB == 4 ? (vf >> s4) & 0x11111111u : 0u;
-        uint32_t a[4], b[4];
-        look_up<KB>(xk, nk, ktab, a[0], a[1]);
-        look_up<KB>(xk >> 16, nk >> 16, ktab, a[2], a[3]);
+        const uint32_t xv = nibbles<VB>(vw, s4), nv = VB == 4 ? (vf >> s4) & 0x11111111u : 0u;
+        uint32_t b[4];
         look_up<VB>(xv, nv, vtab, b[0], b[1]);
         look_up<VB>(xv >> 16, nv >> 16, vtab, b[2], b[3]);
         const uint32_t off = sw128_offset(tok, (grp * 32 + s4 * 8) * 2, 128);
-        *(uint4*)(smem + key_at + off) = make_uint4(a[0], a[1], a[2], a[3]);
         *(uint4*)(smem + val_at + off) = make_uint4(b[0], b[1], b[2], b[3]);
         if (ALG2) {
           const uint32_t z = (sw >> s4) & 0x11111111u;
@@ -314,24 +339,16 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
       }
     }
     fence_proxy_async_smem();
-    tc_fence_before();
     __syncthreads();
-    if (!loaded) {
-      if (!__syncthreads_and(mbar_wait(&bar[0], 0, p.err, kDevTimeoutLoad, abort_flag))) break;
-      loaded = true;
-    }
-    tc_fence_after();
     if (warp == 0 && elect_one_sync()) {
-      const uint32_t m = smem_u32(smem + L::kMat), sg = smem_u32(smem + L::kSgn), k = smem_u32(smem + key_at),
-                     v = smem_u32(smem + val_at), s = smem_u32(smem + L::kS);
+      const uint32_t v = smem_u32(smem + val_at), s = smem_u32(smem + L::kS);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t at = (ks >> 2) * 16384u + (ks & 3) * 32u;
-        mma_f16_ss(tk, desc_kmajor_sw128(k + at), desc_kmajor_sw128(m + at), idesc_f16_f32(128, D), ks > 0);
         mma_f16_ss(tv, desc_kmajor_sw128(m + at), desc_kmajor_sw128(v + at), idesc_f16_f32(128, 128), ks > 0);
         if (ALG2) mma_f16_ss(tv, desc_kmajor_sw128(sg + at), desc_kmajor_sw128(s + at), idesc_f16_f32(128, 128), 1);
       }
-      mma_commit(&bar[1]);
+      mma_commit(&bar[2]);
     }
     __syncwarp();
     const int done = item;
@@ -341,7 +358,6 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
       locate(item + gridDim.x);
     }
     if (!__syncthreads_and(mbar_wait(&bar[1], phase, p.err, kDevTimeoutMma, abort_flag))) break;
-    phase ^= 1;
     tc_fence_after();
     // ---- products into fp16 tiles, in place of the operands -----------------------------------------------
     const int quarter = warp & 3, part = warp >> 2;
@@ -367,6 +383,9 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
               make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
       }
     }
+    if (!__syncthreads_and(mbar_wait(&bar[2], phase, p.err, kDevTimeoutMma, abort_flag))) break;
+    phase ^= 1;
+    tc_fence_after();
     if (quarter * 32 < D) {
       const int row = quarter * 32 + lane;
 #pragma unroll
