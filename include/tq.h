@@ -419,7 +419,7 @@ TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, 
  * tokens, and those past max_kv_len or max_pages, are taken as not seen; a sequence with a bad q_start has no
  * queries, and its outputs are left as they were. A record with a norm that is not finite makes the rows that see
  * it not finite, and no others.
- * Softmax and sums in fp32. A sequence with few query rows per KV head (Qn Hq / Hkv up to 48) meets the codes
+ * Softmax and sums in fp32. A sequence with few query rows per KV head (Qn Hq / Hkv up to 48, up to 256 where B Hkv is small) meets the codes
  * themselves: its queries and the key levels enter the tensor cores as 16-bit integers, value levels and softmax
  * weights as fp16. A longer chunk's visible tokens are decoded once into fp16 tiles in the workspace, by groups of
  * (sequence, KV head) pairs that share 1 GiB of it (one pair at least: 4 d bytes per token).

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kCombThreads) combine_kernel(const __grid_cons
 // ---- host -----------------------------------------------------------------------------------------------
 
 struct Plan {
-  int row_blocks, rows_per_item, ctas;
+  int row_blocks, rows_per_item, ctas, chunk_rows;
   size_t qr, qs, parts, ml, po, total;
   PagedChunkPlan chunk;
 };
@@ -257,8 +257,9 @@ struct Plan {
 Plan plan(const tq_paged_kv* kv, int B, int Hq, int64_t total_q, int max_q, int64_t max_kv, int window) {   // B and max_q > 0
   Plan P{};
   const int g = Hq / kv->Hkv;
-  const bool chunks = (int64_t)max_q * g > kChunkRows;
-  const int rows = chunks ? kChunkRows : max_q * g;
+  P.chunk_rows = paged_chunk_rows(B * kv->Hkv);
+  const bool chunks = (int64_t)max_q * g > P.chunk_rows;
+  const int rows = chunks ? P.chunk_rows : max_q * g;
   P.rows_per_item = rows <= 4 ? 4 : 8;                           // one or two column blocks
   P.row_blocks = (rows + P.rows_per_item - 1) / P.rows_per_item;
   P.ctas = 2 * sm_count();                                       // as many as run at a time
@@ -422,7 +423,7 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   p.po = (float*)(w + P.po);
   p.row_blocks = P.row_blocks;
   p.rows_per_item = P.rows_per_item;
-  p.chunk_rows = kChunkRows;
+  p.chunk_rows = P.chunk_rows;
   p.err = device_error_word();
   if (!p.err) return fail(TQ_ERR_CUDA, f + ": no device error word (is a CUDA device present?)");
   cudaStream_t st = (cudaStream_t)stream;

@@ -1,5 +1,5 @@
 // Attention of chunks (many query rows per KV head) over the paged packed cache: tq_paged_attend's path for
-// sequences with more than kChunkRows rows.
+// sequences with more query rows per KV head than a decode step takes (paged_chunk_rows).
 //
 // Two kernels per group of (sequence, KV head) units:
 //   open   decodes each 128-token tile once, K = n Pi^T c[idx] and V = n (Pi^T c[idx] + alpha gamma S^T (2 z - 1)),
@@ -20,10 +20,8 @@
 // its place, so that no other row meets it.
 //
 // Measured: a chunk of 2048 queries over 8192 tokens (32 heads over 8, V by Algorithm 2) 305 us, 778 TFLOP/s, of which
-// opening takes 27 (512 tiles); twice 2048 over 16384 tokens with a cap 1640 us, 627 TFLOP/s. A step of 256 rows x 128
-// tokens takes about 3700 cycles, of which the tensor cores' operand traffic needs 3072, at 1.4 GHz under load.
-// kChunkRows: eight rows of a decode step cost about what 256 rows cost here, less the opening; at 48 rows the six row
-// blocks of a step read the cache six times.
+// opening takes 25 (512 tiles); twice 2048 over 16384 tokens with a cap 1640 us, 627 TFLOP/s. A step of 256 rows x 128
+// tokens takes about 3700 cycles, five sixths of which the tensor cores' operand traffic needs, at 1.4 GHz under load.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -941,7 +939,7 @@ constexpr int64_t kOpenBytes = (int64_t)1 << 30;
 PagedChunkPlan paged_chunk_plan(const tq_paged_kv* kv, int B, int Hq, int64_t total_q, int max_q, int64_t max_kv, int window) {
   PagedChunkPlan P{};
   const int g = Hq / kv->Hkv;
-  P.slots = (int)std::min<int64_t>(B, total_q * g / (kChunkRows + 1));
+  P.slots = (int)std::min<int64_t>(B, total_q * g / (paged_chunk_rows(B * kv->Hkv) + 1));
   if (max_kv == 0) max_kv = 1;
   const int64_t units = std::max<int64_t>((int64_t)P.slots * kv->Hkv, 1), all = (max_kv + kTile - 1) / kTile;
   const int64_t most = std::min<int64_t>(units, std::max<int64_t>(1, kOpenBytes / (all * (int64_t)tile_bytes(kv->d)))) * all;

@@ -584,6 +584,78 @@ def test_attend_many_times(dev, case):
     assert all(torch.equal(o, outs[0]) for o in outs)
 
 
+def test_attend_on_two_streams_at_once(dev):
+    """Chunks and steps side by side, each with a workspace of its own, as they come and as a pair of captured graphs."""
+    Hq, Hkv, d = 8, 2, 128
+    rng = np.random.default_rng(12)
+    pool = Paged(dev, [3000, 1200, 640], Hkv, d, 3, 3, 2, 64, seed=12)
+    jobs = []
+    for q_lens in ([1, 1, 1], [300, 150, 1]):
+        q = queries(rng, sum(q_lens), Hq, d, dev)
+        want = pool.call(q, q_lens)
+        args = [i32(a, dev) for a in (np.concatenate([[0], np.cumsum(q_lens)]), pool.lens, pool.table)]
+        ws = torch.empty(tq.tq_paged_attend_workspace_bytes(pool.kv, 3, Hq, sum(q_lens), max(q_lens), 3000), dtype=torch.uint8, device=dev)
+        jobs.append((q, want, args, ws, torch.zeros_like(q), max(q_lens), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def go(job):
+        q, want, args, ws, out, most, stream = job
+        tq.tq_paged_attend(pool.kv, q, *args, rotation(d, dev)[2], out, max_q_len=most, max_kv_len=3000, ws=ws)
+
+    for _ in range(20):
+        for job in jobs:
+            with torch.cuda.stream(job[6]):
+                go(job)
+    torch.cuda.synchronize()
+    assert all(torch.equal(job[1], job[4]) for job in jobs)
+    graphs = []
+    for job in jobs:
+        job[4].zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            go(job)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, job in zip(graphs, jobs):
+            with torch.cuda.stream(job[6]):
+                g.replay()
+    torch.cuda.synchronize()
+    tq.tq_sync_check()
+    assert all(torch.equal(job[1], job[4]) for job in jobs)
+
+
+def test_binding_refuses(dev):
+    """What the C side cannot see: dtypes, shapes, layouts and devices of the tensors."""
+    kv = tq.empty_paged(4, 2, 16, 64, 3, 3, device=dev)
+    rot = rotation(64, dev)[2]
+    bf = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=dev)
+    pos, table = torch.zeros(3, dtype=torch.int32, device=dev), tq.tq_rope_table(8, 64)
+    slots = torch.arange(3, device=dev)
+    for bad in (dict(x=bf.double()), dict(positions=pos.long()), dict(positions=pos[:2]), dict(table=table.double()),
+                dict(table=table[:, :, :1]), dict(out=bf.float()), dict(x=bf.transpose(1, 2)), dict(positions=pos.cpu())):
+        with pytest.raises((ValueError, tq.TQError)):
+            tq.tq_rope(**(dict(x=bf, positions=pos, table=table) | bad))
+    for bad in (dict(k_new=bf.half()), dict(v_new=bf.float()), dict(slots=slots.int()), dict(slots=slots[:2]), dict(positions=None),
+                dict(table=None), dict(k_new=torch.zeros(3, 64, 2, dtype=torch.bfloat16, device=dev).transpose(1, 2)),
+                dict(k_new=bf[:, :, :32]), dict(rot=rot.cpu())):
+        with pytest.raises(ValueError):
+            tq.tq_paged_append(**(dict(kv=kv, k_new=bf, v_new=bf, slots=slots, rot=rot, positions=pos, table=table) | bad))
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device=dev)
+    start, lens, pages = i32([0, 1, 3], dev), i32([5, 9], dev), i32([[0], [1]], dev)
+    for bad in (dict(q=q.float()), dict(q=q[:, :, :32]), dict(out=q[:2]), dict(q_start=start[:2]), dict(kv_len=lens.long()),
+                dict(page_table=pages[0]), dict(prefix_len=lens[:1]), dict(slopes=torch.zeros(3, device=dev)),
+                dict(ws=torch.zeros(1 << 20, dtype=torch.uint8)), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1))):
+        with pytest.raises((ValueError, IndexError)):
+            tq.tq_paged_attend(**(dict(kv=kv, q=q, q_start=start, kv_len=lens, page_table=pages, rot=rot, out=torch.empty_like(q),
+                                       max_q_len=2, max_kv_len=16) | bad))
+    with pytest.raises(ValueError):
+        tq.PagedKV(tq.tq_codebook_init(64, 3), tq.tq_codebook_init(64, 2), kv.tensors[0], kv.tensors[1].float(), *kv.tensors[2:])
+    with pytest.raises(ValueError):
+        tq.PagedKV(tq.tq_codebook_init(64, 3), tq.tq_codebook_init(64, 2), *kv.tensors[:5])
+    tq.tq_sync_check()
+
+
 def test_attend_dirty_workspace_and_single_rows(dev):
     """A workspace of NaN bytes, one token, one query of one head."""
     pool = Paged(dev, [1, 3], 1, 64, 1, 2, 2, 16, seed=1)
