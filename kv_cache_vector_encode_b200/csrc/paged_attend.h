@@ -180,9 +180,10 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 
 // cap tanh(x / cap) in log2 units, from x2 = 2 log2(e) x / cap: tanh(u) = 1 - 2 / (e^(2u) + 1). Its error is
-// absolute, about 2^-23 of the cap, which is what a softmax needs of its scores.
+// absolute, about 2^-23 of the cap, which is what a softmax needs of its scores. e^(2u) may overflow: the quotient is
+// then 0. NaN stays.
 __device__ __forceinline__ float capped(float x2, float cap_log2) {
-  return cap_log2 - __fdividef(2.0f * cap_log2, ex2_approx(fminf(x2, 100.0f)) + 1.0f);
+  return cap_log2 - __fdividef(2.0f * cap_log2, ex2_approx(x2) + 1.0f);
 }
 #endif
 

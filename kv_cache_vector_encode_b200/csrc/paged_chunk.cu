@@ -724,6 +724,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int pos = (int)x.first + jq;
     // ---- this row's query: fp16 times a power of two (exact for what lies within 2^-26 of its largest) -----
     float fac;
+    bool fine;
     {
       const uint4* src = (const uint4*)(p.q + (int64_t)(x.sq.q0 + jq) * p.q_stride + (int64_t)h * D);
       uint4 w[D / 8];
@@ -735,6 +736,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) most = max(most, max(v[k] & 0x7FFFu, (v[k] >> 16) & 0x7FFFu));
       }
+      fine = most < 0x7F80u;
       const int e = min(max((int)(most >> 7), 20), 230);
       const float up = __int_as_float((254 + 11 - e) << 23);
       fac = p.scale_log2 * __int_as_float((e - 11) << 23);
@@ -852,6 +854,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (n > 0 && ok) ok = wait_soon(&bar[O_FULL + u], 0, p.err, kDevTimeoutMma, abort_flag);
     if (ok) {
       tc_fence_after();
+      if (n > 0 && !(fine && fabsf(slope) < INFINITY)) sum = __int_as_float(0x7FC00000);   // the cap and the polynomial may have hidden it
       const float inv = sum == 0.f ? 0.f : __int_as_float((127 - kBits) << 23) / sum;
       uint4* dst = (uint4*)(p.out + ((int64_t)(x.sq.q0 + jq) * p.Hq + h) * D);
 #pragma unroll

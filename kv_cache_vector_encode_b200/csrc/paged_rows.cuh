@@ -431,7 +431,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float nk = __half2float(__ushort_as_half(kn[r + 8 * k]));
-            const float nv = __half2float(__ushort_as_half(vn[r + 8 * k]));
+            // a key norm that is not finite makes the token's value NaN: its score alone might be taken to the cap, or to
+            // minus infinity and a weight of 0
+            const float nv = fmaf(nk, 0.f, __half2float(__ushort_as_half(vn[r + 8 * k])));
             const float ng = ALG2 ? __half2float(__ushort_as_half(((const uint16_t*)(st + L::kVg))[r + 8 * k])) : 0.f;
 #pragma unroll
             for (int u = 0; u < NB; ++u) {

@@ -468,6 +468,44 @@ def test_attend_norms_far_apart(dev, q_lens):
     pool.upload()
 
 
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("q_lens", [[1, 1], [180, 150]])
+def test_attend_not_finite(dev, q_lens, softcap):
+    """Norms and queries that are not finite, with and without a cap (which would take an infinite score to a finite
+    one): the rows that see or hold them are not finite whatever the sign of a score, and no others."""
+    lens, Hq, Hkv, d = [400, 333], 4, 2, 128
+    rng = np.random.default_rng(2)
+    pool = Paged(dev, lens, Hkv, d, 3, 3, 2, 16, seed=4)
+    q = queries(rng, sum(q_lens), Hq, d, dev)
+    good = pool.call(q, q_lens, window=60, softcap=softcap).double().cpu().numpy()
+    assert np.all(np.isfinite(good))
+    n0, pos = q_lens[0], lens[0] - q_lens[0] + np.arange(q_lens[0])
+    for which, what in ((1, np.nan), (1, np.inf), (3, np.nan), (3, np.inf), (5, np.nan), (5, np.inf)):
+        for t in (lens[0] - 60, lens[0] - 9):                    # both seen by the last query
+            keep = pool.host[which].copy()
+            pool.host[which][pool.table[0, t // 16], 1, t % 16] = what
+            pool.upload()
+            got = pool.call(q, q_lens, window=60, softcap=softcap).double().cpu().numpy()
+            tq.tq_sync_check()
+            hit = np.zeros((got.shape[0], Hq), bool)
+            hit[:n0, 2:] = ((t <= pos) & (t > pos - 60))[:, None]
+            assert hit.any()
+            assert not np.any(np.isfinite(got).all(-1)[hit])
+            assert np.array_equal(got[~hit], good[~hit])
+            pool.host[which] = keep
+    pool.upload()
+    for what in (np.nan, np.inf, -np.inf):
+        for window in (1, 60):                                   # one token seen, and many
+            for row in range(0, n0, 7):
+                bad = q.clone()
+                bad[row, 1, 3] = what
+                got = pool.call(bad, q_lens, window=window, softcap=softcap).double().cpu().numpy()
+                ok = np.ones(got.shape[:2], bool)
+                ok[row, 1] = False
+                assert not np.isfinite(got[row, 1]).all()
+                assert np.all(np.isfinite(got[ok]))
+
+
 @pytest.mark.parametrize("q_lens", [[1, 1, 1], [140, 70, 1]])
 def test_attend_reports_bad_pages_and_lengths(dev, q_lens):
     """A page number out of range is reported and its tokens are not seen."""
