@@ -59,13 +59,8 @@ def dequant(codes: np.ndarray, norms: np.ndarray, levels: np.ndarray, Pi: np.nda
     return norms.astype(np.float64)[:, None] * x
 
 
-def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, kv_len: int, scale: float, softcap: float = 0.0, window: int = 0,
-           prefix: int = 0, slopes: np.ndarray | None = None, present: np.ndarray | None = None):
-    """One sequence: q [Qn, Hq, d], k / v [Hkv, kv_len, d] -> out [Qn, Hq, d] and, for error bounds, the weighted
-    length of the values sum_t p_t |v_t| and the largest scale |q| |k_t| of the seen tokens, both [Qn, Hq]."""
-    Qn, Hq, d = q.shape
-    Hkv = k.shape[0]
-    g = Hq // Hkv
+def visible(Qn: int, kv_len: int, window: int = 0, prefix: int = 0, present: np.ndarray | None = None):
+    """Positions [Qn] of the newest Qn of kv_len tokens, and which tokens each sees [Qn, kv_len]."""
     t = np.arange(kv_len)
     pos = kv_len - Qn + np.arange(Qn)
     seen = t[None] <= pos[:, None]
@@ -74,10 +69,19 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, kv_len: int, scale: floa
     seen |= t[None] < prefix
     if present is not None:
         seen &= present[None]
-    out, size, reach = np.zeros((Qn, Hq, d)), np.zeros((Qn, Hq)), np.zeros((Qn, Hq))
+    return pos, seen
+
+
+def softmax_weights(q: np.ndarray, k: np.ndarray, kv_len: int, scale: float, softcap: float = 0.0, window: int = 0,
+                    prefix: int = 0, slopes: np.ndarray | None = None, present: np.ndarray | None = None) -> np.ndarray:
+    """Weights [Qn, Hq, kv_len] of one sequence: q [Qn, Hq, d], k [Hkv, kv_len, d]; 0 for what a query does not see."""
+    Qn, Hq, d = q.shape
+    g = Hq // k.shape[0]
+    pos, seen = visible(Qn, kv_len, window, prefix, present)
+    t = np.arange(kv_len)
+    out = np.zeros((Qn, Hq, kv_len))
     for h in range(Hq):
-        kh, vh = k[h // g], v[h // g]
-        x = scale * (q[:, h].astype(np.float64) @ kh.T)
+        x = scale * (q[:, h].astype(np.float64) @ k[h // g].T)
         if softcap:
             x = softcap * np.tanh(x / softcap)
         if slopes is not None:
@@ -86,7 +90,21 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, kv_len: int, scale: floa
         top = x.max(-1, keepdims=True, initial=-np.inf)
         p = np.where(seen, np.exp(x - np.where(np.isfinite(top), top, 0.0)), 0.0)
         total = p.sum(-1, keepdims=True)
-        p = np.where(total > 0, p / np.where(total > 0, total, 1.0), 0.0)
+        out[:, h] = np.where(total > 0, p / np.where(total > 0, total, 1.0), 0.0)
+    return out
+
+
+def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, kv_len: int, scale: float, softcap: float = 0.0, window: int = 0,
+           prefix: int = 0, slopes: np.ndarray | None = None, present: np.ndarray | None = None):
+    """One sequence: q [Qn, Hq, d], k / v [Hkv, kv_len, d] -> out [Qn, Hq, d] and, for error bounds, the weighted
+    length of the values sum_t p_t |v_t| and the largest scale |q| |k_t| of the seen tokens, both [Qn, Hq]."""
+    Qn, Hq, d = q.shape
+    g = Hq // k.shape[0]
+    w = softmax_weights(q, k, kv_len, scale, softcap, window, prefix, slopes, present)
+    out, size, reach = np.zeros((Qn, Hq, d)), np.zeros((Qn, Hq)), np.zeros((Qn, Hq))
+    _, seen = visible(Qn, kv_len, window, prefix, present)
+    for h in range(Hq):
+        kh, vh, p = k[h // g], v[h // g], w[:, h]
         out[:, h] = p @ vh
         size[:, h] = p @ np.linalg.norm(vh, axis=1)
         if kv_len:

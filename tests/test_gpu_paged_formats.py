@@ -1,0 +1,86 @@
+"""tq_paged_attend in every packed format and form of its kernels, held to the bound of tests/paged_bound.py (B200).
+
+A decode step's kernel exists per head size, key bits, value bits, algorithm and number of rows (up to four, more), the
+chunks' per head size, key bits, value bits and algorithm: each runs here once at least."""
+import math
+
+import numpy as np
+import pytest
+
+import paged_bound as PB
+from test_gpu_paged import CASES, Paged, i32, queries, rotation
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+tq = pytest.importorskip("kv_cache_vector_encode_b200")
+
+
+@pytest.fixture(scope="module")
+def dev(gpu_required):
+    tq.lib()
+    return torch.device("cuda")
+
+
+def check(pool, out, q, q_lens, scale=None, prefix=None, present=None, **kw):
+    got, qs = out.double().cpu().numpy(), q.double().cpu().numpy()
+    start = np.concatenate([[0], np.cumsum(q_lens)])
+    assert np.all(np.isnan(got[start[-1]:]))                     # padding rows as they were
+    Pi = rotation(pool.d, pool.dev)[0]
+    for b, m in enumerate(q_lens):
+        if not m:
+            continue
+        k, v = pool.sequence(b)
+        here = None if present is None else present[b]
+        if here is not None:
+            k, v = (np.where(here[None, :, None], a, 0.0) for a in (k, v))
+        rows = slice(start[b], start[b + 1])
+        want, tol, sees = PB.bounds(qs[rows], k, v, Pi, pool.lens[b], scale or 1.0 / math.sqrt(pool.d),
+                                    prefix=0 if prefix is None else prefix[b], present=here, **kw)
+        err = np.linalg.norm(got[rows] - want, axis=-1)
+        assert np.all(err <= tol), (b, float(np.max(err / np.maximum(tol, 1e-30))))
+        assert np.all(got[rows][~sees] == 0)
+
+
+@pytest.mark.parametrize("vb,alg", [(1, 1), (2, 1), (3, 1), (4, 1), (2, 2), (3, 2), (4, 2)])
+@pytest.mark.parametrize("kb", [1, 2, 3, 4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_formats(dev, d, kb, vb, alg):
+    number = 7 * kb + vb + 3 * alg + d // 64
+    lens, Hq, Hkv = [150, 37], 8, 2
+    pool = Paged(dev, lens, Hkv, d, kb, vb, alg, 16 << number % 7, seed=number)
+    rng = np.random.default_rng(number)
+    # four rows per KV head; eight of one sequence, and a chunk of 280 of another
+    for q_lens in ([1, 1], [70, 2]):
+        q = queries(rng, sum(q_lens) + 2, Hq, d, dev)
+        for opt in ({}, dict(scale=0.3), dict(window=19, softcap=4.0)):
+            out = pool.call(q, q_lens, pad=2, **opt)
+            tq.tq_sync_check()
+            check(pool, out, q, q_lens, **opt)
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attend_closely(dev, case):
+    lens, q_lens, Hq, Hkv, d, kb, vb, alg, ps, opt = CASES[case]
+    rng = np.random.default_rng(case)
+    pool = Paged(dev, lens, Hkv, d, kb, vb, alg, ps, seed=100 + case)
+    q = queries(rng, sum(q_lens) + 2, Hq, d, dev)
+    opt = dict(opt)
+    if opt.pop("prefix", False):
+        opt["prefix"] = [min(n, int(rng.integers(0, n + 1))) for n in lens]
+    if opt.pop("slopes", False):
+        opt["slopes"] = (2.0 ** (-8.0 * np.arange(1, Hq + 1) / Hq)).astype(np.float32)
+    out = pool.call(q, q_lens, pad=2, **opt)
+    tq.tq_sync_check()
+    check(pool, out, q, q_lens, **opt)
+
+
+def test_attend_long_context(dev):
+    """One sequence alone, and contexts as long as the packed cache's other calls are measured at."""
+    for lens, Hq, Hkv, ps in (([131072], 8, 2, 64), ([50001, 131000], 4, 1, 256)):
+        pool = Paged(dev, lens, Hkv, 128, 3, 2, 2, ps, seed=9)
+        q_lens = [1] * len(lens)
+        q = queries(np.random.default_rng(9), len(lens), Hq, 128, dev)
+        out = pool.call(q, q_lens)
+        tq.tq_sync_check()
+        check(pool, out, q, q_lens)
