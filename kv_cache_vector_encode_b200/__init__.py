@@ -14,6 +14,7 @@ Names follow the C ABI. Tensors:
   rot      uint8 buffer of tq_rotation_bytes(d) bytes (prepared by tq_rotation_prepare)
   table    [n_pos, rot_dim/2, 2] float32 (cos, sin) of tq_rope_table
   PagedKV  the packed cache in pages: the arrays above with leading axes [pages, Hkv, page_size]
+  ws       uint8 workspace; a call that is given none takes one from the pool of the stream it launches on
 """
 from __future__ import annotations
 
@@ -144,6 +145,25 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _empty(shape, dtype, device, stream, keep=False):
+    """torch.empty for a call that launches on `stream`: memory of that stream, so that what it waits for, and what may
+    follow when it is released (a workspace when the call returns), is in that stream's order. keep: the tensor is the
+    call's result, which the current stream may go on using until it is released."""
+    import torch
+    if stream is not None and device.type == "cuda":
+        current = torch.cuda.current_stream(device)
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle != current.cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(handle, device=device)
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            if keep:
+                t.record_stream(current)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t, name, dtypes=None, allow_none=False):
     if t is None:
         if allow_none:
@@ -185,7 +205,7 @@ def tq_rotation_prepare(Pi, S, rot=None, stream=None):
     d = Pi.shape[0]
     nbytes = tq_rotation_bytes(d)
     if rot is None:
-        rot = torch.empty(nbytes, dtype=torch.uint8, device=Pi.device)
+        rot = _empty(nbytes, torch.uint8, Pi.device, stream, keep=True)
     _check(lib().tq_rotation_prepare(d, _ptr(Pi, "Pi", [torch.float32]), _ptr(S, "S", [torch.float32]),
                                      _ptr(rot, "rot"), rot.numel(), _stream(stream)))
     return rot
@@ -208,7 +228,7 @@ def tq_encode_prod(cb_bm1: Codebook, x, rot, codes, signs, norms, gammas, ws=Non
     n, d = x.shape
     wsb = tq_encode_workspace_bytes(n, d, 2)
     if ws is None and wsb > 0:
-        ws = torch.empty(wsb, dtype=torch.uint8, device=x.device)
+        ws = _empty(wsb, torch.uint8, x.device, stream)
     _check(lib().tq_encode_prod(ctypes.byref(cb_bm1), n, d, _ptr(x, "x", [torch.float32, torch.bfloat16]),
                                 _xdtype(x), _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
                                 _ptr(signs, "signs", [torch.int32]), _ptr(norms, "norms", [torch.float16]),
@@ -274,7 +294,7 @@ def tq_scores(cb: Codebook, q, rot, codes, norms, signs=None, gammas=None, score
     n = norms.shape[0]
     wsb = tq_scores_workspace_bytes(nq, n, d, k)
     if ws is None:
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
+        ws = _empty(max(wsb, 16), torch.uint8, q.device, stream)
     _check(lib().tq_scores(ctypes.byref(cb), nq, n, d, _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q),
                            _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
                            _ptr(signs, "signs", [torch.int32], True), _ptr(norms, "norms", [torch.float16]),
@@ -298,7 +318,7 @@ def tq_attend_decode(cb_k: Codebook, cb_v: Codebook, q, rot, k_codes, k_norms, v
         scale = 0.0                   # the library's default, 1/sqrt(d)
     wsb = tq_attend_workspace_bytes(B, Hq, Hkv, T, d)
     if ws is None:
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
+        ws = _empty(max(wsb, 16), torch.uint8, q.device, stream)
     _check(lib().tq_attend_decode(ctypes.byref(cb_k), ctypes.byref(cb_v), B, Hq, Hkv, T, d,
                                   _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _ptr(rot, "rot"),
                                   _ptr(k_codes, "k_codes", [torch.int32]), _ptr(k_norms, "k_norms", [torch.float16]),
@@ -347,7 +367,7 @@ def tq_attend_prefill(cb_k: Codebook, cb_v: Codebook, q, rot, k_codes, k_norms, 
         scale = 0.0                   # the library's default, 1/sqrt(d)
     wsb = tq_attend_prefill_workspace_bytes(B, Hq, Hkv, Qn, T, d)
     if ws is None:
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
+        ws = _empty(max(wsb, 16), torch.uint8, q.device, stream)
     _check(lib().tq_attend_prefill(ctypes.byref(cb_k), ctypes.byref(cb_v), B, Hq, Hkv, Qn, T, d,
                                    _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _ptr(rot, "rot"),
                                    _ptr(k_codes, "k_codes", [torch.int32]), _ptr(k_norms, "k_norms", [torch.float16]),
@@ -383,7 +403,7 @@ def tq_attend_append(cb_k: Codebook, cb_v: Codebook, q, rot, k_new, v_new, T_cur
         scale = 0.0                   # the library's default, 1/sqrt(d)
     wsb = tq_attend_append_workspace_bytes(B, Hq, Hkv, T_cur, d, cb_k.bits, cb_v.bits)
     if ws is None:
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
+        ws = _empty(max(wsb, 16), torch.uint8, q.device, stream)
     _check(lib().tq_attend_append(ctypes.byref(cb_k), ctypes.byref(cb_v), B, Hq, Hkv, T_cur, T_max, d,
                                   _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q),
                                   _ptr(k_new, "k_new", [torch.float32, torch.bfloat16]),
@@ -462,7 +482,7 @@ def tq_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: int 
     """Table [n_pos, rot_dim // 2, 2] float32 of (cos, sin) for tq_rope and tq_paged_append."""
     import torch
     device = torch.device(device)
-    table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    table = _empty((n_pos, rot_dim // 2, 2), torch.float32, device, stream, keep=True)
     _current(table, "device")
     _check(lib().tq_rope_table(n_pos, rot_dim, base, scaling, factor, low_turns, high_turns, original_len, magnitude,
                                table.data_ptr(), _stream(stream)))
@@ -592,8 +612,8 @@ def tq_paged_attend(kv: PagedKV, q, q_start, kv_len, page_table, rot, out, max_q
     slope = None if slopes is None else _in(slopes, "slopes", device, _tc.f32, Hq)
     if ws is None:
         import torch
-        ws = torch.empty(max(tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len), 16),
-                         dtype=torch.uint8, device=q.device)
+        ws = _empty(max(tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len), 16), torch.uint8,
+                    q.device, stream)
     elif ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous and on device {device}")
     status = _lib.tq_paged_attend(kv.ref, B, Hq, total_q, max_q_len, max_kv_len, q.data_ptr(), qt if total_q > 1 else Hq * d,
