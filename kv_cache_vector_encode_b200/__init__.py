@@ -178,6 +178,15 @@ def _ptr(t, name, dtypes=None, allow_none=False):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _rotation(rot, d):
+    """Address of a prepared rotation that is as large as one for d (the C calls take no size)."""
+    import torch
+    ptr = _ptr(rot, "rot", [torch.uint8])
+    if rot.numel() < tq_rotation_bytes(d):
+        raise ValueError(f"rot has {rot.numel()} bytes, a rotation prepared for d = {d} has {tq_rotation_bytes(d)}")
+    return ptr
+
+
 def _xdtype(t):
     import torch
     return {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}[t.dtype]
@@ -203,6 +212,8 @@ def tq_rotation_prepare(Pi, S, rot=None, stream=None):
     """Prepare the rotation buffer from device fp32 Pi, S (d x d); returns it."""
     import torch
     d = Pi.shape[0]
+    if tuple(Pi.shape) != (d, d) or tuple(S.shape) != (d, d):
+        raise ValueError("Pi and S must be [d, d]")
     nbytes = tq_rotation_bytes(d)
     if rot is None:
         rot = _empty(nbytes, torch.uint8, Pi.device, stream, keep=True)
@@ -215,7 +226,7 @@ def tq_encode_mse(cb: Codebook, x, rot, codes, norms, stream=None):
     import torch
     n, d = x.shape
     _check(lib().tq_encode_mse(ctypes.byref(cb), n, d, _ptr(x, "x", [torch.float32, torch.bfloat16]), _xdtype(x),
-                               _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
+                               _rotation(rot, d), _ptr(codes, "codes", [torch.int32]),
                                _ptr(norms, "norms", [torch.float16]), _stream(stream)))
 
 
@@ -230,7 +241,7 @@ def tq_encode_prod(cb_bm1: Codebook, x, rot, codes, signs, norms, gammas, ws=Non
     if ws is None and wsb > 0:
         ws = _empty(wsb, torch.uint8, x.device, stream)
     _check(lib().tq_encode_prod(ctypes.byref(cb_bm1), n, d, _ptr(x, "x", [torch.float32, torch.bfloat16]),
-                                _xdtype(x), _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
+                                _xdtype(x), _rotation(rot, d), _ptr(codes, "codes", [torch.int32]),
                                 _ptr(signs, "signs", [torch.int32]), _ptr(norms, "norms", [torch.float16]),
                                 _ptr(gammas, "gammas", [torch.float16]), _ptr(ws, "ws", None, True),
                                 ws.numel() if ws is not None else 0, _stream(stream)))
@@ -239,7 +250,7 @@ def tq_encode_prod(cb_bm1: Codebook, x, rot, codes, signs, norms, gammas, ws=Non
 def tq_decode(cb: Codebook, rot, codes, norms, out, signs=None, gammas=None, stream=None):
     import torch
     n, d = out.shape
-    _check(lib().tq_decode(ctypes.byref(cb), n, d, _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
+    _check(lib().tq_decode(ctypes.byref(cb), n, d, _rotation(rot, d), _ptr(codes, "codes", [torch.int32]),
                            _ptr(signs, "signs", [torch.int32], True), _ptr(norms, "norms", [torch.float16]),
                            _ptr(gammas, "gammas", [torch.float16], True),
                            _ptr(out, "out", [torch.float32, torch.bfloat16]), _xdtype(out), _stream(stream)))
@@ -270,7 +281,7 @@ def tq_encode_mse_mixed(group_bits, x, rot, codes, norms, stream=None):
     n, d = x.shape
     cbs, gb = _mixed_args(d, group_bits)
     _check(lib().tq_encode_mse_mixed(cbs, gb, n, d, _ptr(x, "x", [torch.float32, torch.bfloat16]), _xdtype(x),
-                                     _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
+                                     _rotation(rot, d), _ptr(codes, "codes", [torch.int32]),
                                      _ptr(norms, "norms", [torch.float16]), _stream(stream)))
 
 
@@ -278,7 +289,7 @@ def tq_decode_mixed(group_bits, rot, codes, norms, out, stream=None):
     import torch
     n, d = out.shape
     cbs, gb = _mixed_args(d, group_bits)
-    _check(lib().tq_decode_mixed(cbs, gb, n, d, _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
+    _check(lib().tq_decode_mixed(cbs, gb, n, d, _rotation(rot, d), _ptr(codes, "codes", [torch.int32]),
                                  _ptr(norms, "norms", [torch.float16]),
                                  _ptr(out, "out", [torch.float32, torch.bfloat16]), _xdtype(out), _stream(stream)))
 
@@ -296,7 +307,7 @@ def tq_scores(cb: Codebook, q, rot, codes, norms, signs=None, gammas=None, score
     if ws is None:
         ws = _empty(max(wsb, 16), torch.uint8, q.device, stream)
     _check(lib().tq_scores(ctypes.byref(cb), nq, n, d, _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q),
-                           _ptr(rot, "rot"), _ptr(codes, "codes", [torch.int32]),
+                           _rotation(rot, d), _ptr(codes, "codes", [torch.int32]),
                            _ptr(signs, "signs", [torch.int32], True), _ptr(norms, "norms", [torch.float16]),
                            _ptr(gammas, "gammas", [torch.float16], True),
                            _ptr(scores, "scores", [torch.float32], True), k,
@@ -320,7 +331,7 @@ def tq_attend_decode(cb_k: Codebook, cb_v: Codebook, q, rot, k_codes, k_norms, v
     if ws is None:
         ws = _empty(max(wsb, 16), torch.uint8, q.device, stream)
     _check(lib().tq_attend_decode(ctypes.byref(cb_k), ctypes.byref(cb_v), B, Hq, Hkv, T, d,
-                                  _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _ptr(rot, "rot"),
+                                  _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _rotation(rot, d),
                                   _ptr(k_codes, "k_codes", [torch.int32]), _ptr(k_norms, "k_norms", [torch.float16]),
                                   _ptr(k_signs, "k_signs", [torch.int32], True),
                                   _ptr(k_gammas, "k_gammas", [torch.float16], True),
@@ -340,7 +351,7 @@ def tq_attend_decode_noalloc(cb_k: Codebook, cb_v: Codebook, q, rot, k_codes, k_
     if scale is None:
         scale = 0.0                   # the library's default, 1/sqrt(d)
     _check(lib().tq_attend_decode_noalloc(ctypes.byref(cb_k), ctypes.byref(cb_v), B, Hq, Hkv, T, d,
-                                          _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _ptr(rot, "rot"),
+                                          _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _rotation(rot, d),
                                           _ptr(k_codes, "k_codes", [torch.int32]),
                                           _ptr(k_norms, "k_norms", [torch.float16]),
                                           _ptr(k_signs, "k_signs", [torch.int32], True),
@@ -369,7 +380,7 @@ def tq_attend_prefill(cb_k: Codebook, cb_v: Codebook, q, rot, k_codes, k_norms, 
     if ws is None:
         ws = _empty(max(wsb, 16), torch.uint8, q.device, stream)
     _check(lib().tq_attend_prefill(ctypes.byref(cb_k), ctypes.byref(cb_v), B, Hq, Hkv, Qn, T, d,
-                                   _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _ptr(rot, "rot"),
+                                   _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q), _rotation(rot, d),
                                    _ptr(k_codes, "k_codes", [torch.int32]), _ptr(k_norms, "k_norms", [torch.float16]),
                                    _ptr(k_signs, "k_signs", [torch.int32], True),
                                    _ptr(k_gammas, "k_gammas", [torch.float16], True),
@@ -408,7 +419,7 @@ def tq_attend_append(cb_k: Codebook, cb_v: Codebook, q, rot, k_new, v_new, T_cur
                                   _ptr(q, "q", [torch.float32, torch.bfloat16]), _xdtype(q),
                                   _ptr(k_new, "k_new", [torch.float32, torch.bfloat16]),
                                   _ptr(v_new, "v_new", [torch.float32, torch.bfloat16]), _xdtype(k_new),
-                                  _ptr(rot, "rot"), _ptr(k_codes, "k_codes", [torch.int32]),
+                                  _rotation(rot, d), _ptr(k_codes, "k_codes", [torch.int32]),
                                   _ptr(k_norms, "k_norms", [torch.float16]), _ptr(v_codes, "v_codes", [torch.int32]),
                                   _ptr(v_signs, "v_signs", [torch.int32]), _ptr(v_norms, "v_norms", [torch.float16]),
                                   _ptr(v_gammas, "v_gammas", [torch.float16]), float(scale),
@@ -424,8 +435,8 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.f32, self.bf16, self.f16, self.i32, self.i64 = (torch.float32, torch.bfloat16, torch.float16, torch.int32,
-                                                             torch.int64)
+        self.f32, self.bf16, self.f16 = torch.float32, torch.bfloat16, torch.float16
+        self.i32, self.i64, self.u8 = torch.int32, torch.int64, torch.uint8
         self.code = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
         self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -536,6 +547,7 @@ class PagedKV:
         self.tensors = (k_codes, k_norms, v_codes, v_norms, v_signs, v_gammas)
         self.num_pages, self.Hkv, self.page_size = at
         self.d = 32 * groups
+        self.rot_bytes = tq_rotation_bytes(self.d)
         self.struct = _PagedKV()
         ptr = [None if t is None else t.data_ptr() for t in (k_codes, k_norms, v_codes, v_signs, v_norms, v_gammas)]
         _check(lib().tq_paged_kv_init(ctypes.byref(cb_k), ctypes.byref(cb_v), self.d, self.Hkv, self.page_size,
@@ -572,14 +584,15 @@ def tq_paged_append(kv: PagedKV, k_new, v_new, slots, rot, positions=None, table
     elif positions is not None or table is not None:
         raise ValueError("positions and table go together")
     status = _lib.tq_paged_append(kv.ref, tokens, k_new.data_ptr(), strides[0], v_new.data_ptr(), strides[1], _tc.code[dtype],
-                                  at, pos, tab, n_pos, rot_dim, layout, _prepared(rot, device), _raw(stream, device))
+                                  at, pos, tab, n_pos, rot_dim, layout, _prepared(rot, kv), _raw(stream, device))
     if status:
         _check(status)
 
 
-def _prepared(rot, device):
-    if rot.get_device() != device:
-        raise ValueError(f"rot must be on device {device}")
+def _prepared(rot, kv):
+    """Address of a rotation prepared for the cache's d, which its size tells."""
+    if rot.get_device() != kv.device or rot.dtype is not _tc.u8 or rot.numel() != kv.rot_bytes or not rot.is_contiguous():
+        raise ValueError(f"rot must be a rotation prepared for d = {kv.d}: {kv.rot_bytes} contiguous torch.uint8 on device {kv.device}")
     return rot.data_ptr()
 
 
@@ -618,7 +631,7 @@ def tq_paged_attend(kv: PagedKV, q, q_start, kv_len, page_table, rot, out, max_q
         raise ValueError(f"ws must be contiguous and on device {device}")
     status = _lib.tq_paged_attend(kv.ref, B, Hq, total_q, max_q_len, max_kv_len, q.data_ptr(), qt if total_q > 1 else Hq * d,
                                   TQ_BF16, start, lens, pages, max_pages, scale or 0.0, softcap, window, prefix, slope,
-                                  _prepared(rot, device), out_ptr, ws.data_ptr(), ws.nbytes, _raw(stream, device))
+                                  _prepared(rot, kv), out_ptr, ws.data_ptr(), ws.nbytes, _raw(stream, device))
     if status:
         _check(status)
     return out
