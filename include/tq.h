@@ -442,10 +442,10 @@ TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, int32_t Hq, i
  * before. Nothing faults and nothing hangs. Errors: INVALID_ARG (limit), CUDA. */
 TQ_API tq_status tq_selftest_wait(uint64_t limit_ns, void* stream);
 
-/* Synchronises `stream`, then reports a pending CUDA error (TQ_ERR_CUDA) or a device-side
- * timeout recorded by any libtq kernel since the last check (TQ_ERR_DEVICE_TIMEOUT) or an index
- * outside its range that a kernel met in device data (TQ_ERR_DEVICE_INPUT); it clears what it
- * reports. TQ_OK otherwise. */
+/* Synchronises `stream`, then reports a pending CUDA error (TQ_ERR_CUDA), or what any libtq kernel
+ * recorded since it was last reported: a bounded wait that gave up (TQ_ERR_DEVICE_TIMEOUT), or an
+ * index outside its range in device data (TQ_ERR_DEVICE_INPUT). One of them per call, the timeout
+ * first; a call clears what it reports, and the next one reports the other. TQ_OK otherwise. */
 TQ_API tq_status tq_sync_check(void* stream);
 
 #ifdef __cplusplus

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     const AppendTile<D> tile{p, (value ? item : item - p.tiles) * kVec, value};
     int64_t rec = -1;                                            // record number
     if (in.slot >= p.slots_total || (in.slot >= 0 && p.half && (in.pos < 0 || in.pos >= p.n_pos)))
-      atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+      report_bad_input(p.err);
     else if (in.slot >= 0)
       rec = (((in.slot >> p.page_shift) * p.Hkv + in.h) << p.page_shift) + (in.slot & ((1 << p.page_shift) - 1));
     float x[32];

@@ -123,7 +123,7 @@ __device__ __forceinline__ PagedSeq paged_seq_quiet(const PagedAttendParams& p, 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b) {
   bool bad;
   const PagedSeq s = paged_seq_checked(p, b, bad);
-  if (bad && threadIdx.x == 0) atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+  if (bad && threadIdx.x == 0) report_bad_input(p.err);
   return s;
 }
 

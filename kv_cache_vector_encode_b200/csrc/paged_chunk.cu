@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
         vg = __ldg(p.v_gammas + rec);
       }
     } else if (next_lo) {
-      atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+      report_bad_input(p.err);
     }
   };
 

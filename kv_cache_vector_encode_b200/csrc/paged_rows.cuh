@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
           if (blk < nblk) {
             uint32_t bytes = 16;
             if ((uint32_t)page >= (uint32_t)p.num_pages) {
-              if (lane == 0) atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+              if (lane == 0) report_bad_input(p.err);
               absent |= 1u << s;
               page = 0;
               bytes = 0;

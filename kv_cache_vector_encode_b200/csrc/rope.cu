@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
   const int32_t pos = p.positions[t];
   if (pos < 0) return;
   if (pos >= p.n_pos) {
-    atomicCAS(p.err, 0u, (uint32_t)kDevBadInput);
+    report_bad_input(p.err);
     return;
   }
   const T* x = (const T*)p.x + t * p.xt;

@@ -14,7 +14,7 @@
 
 namespace tq {
 
-__device__ uint32_t g_device_error = 0;
+__device__ uint32_t g_device_error[2] = {0, 0};
 
 RotLayout rot_layout(int d) {
   RotLayout L{};
@@ -170,13 +170,15 @@ extern "C" TQ_API tq_status tq_sync_check(void* stream) {
   clear_error();
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "tq_sync_check");
-  uint32_t v = 0, zero = 0;
-  if ((e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(v))) != cudaSuccess) return cuda_fail(e, "tq_sync_check");
-  if (v != 0) {
-    cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero));
-    if (v == kDevBadInput)
-      return fail(TQ_ERR_DEVICE_INPUT, "a libtq kernel met a position, slot, page or length out of range");
-    return fail(TQ_ERR_DEVICE_TIMEOUT, "a libtq kernel gave up a bounded wait (device code " + std::to_string(v) + ")");
+  uint32_t v[2] = {0, 0};
+  const uint32_t zero = 0;
+  if ((e = cudaMemcpyFromSymbol(v, g_device_error, sizeof(v))) != cudaSuccess) return cuda_fail(e, "tq_sync_check");
+  for (int i = 0; i < 2; ++i) {   // one report per call, a timeout first; the other stays pending
+    if (v[i] == 0) continue;
+    if ((e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero), i * sizeof(zero))) != cudaSuccess)
+      return cuda_fail(e, "tq_sync_check");
+    return i == 0 ? fail(TQ_ERR_DEVICE_TIMEOUT, "a libtq kernel gave up a bounded wait (device code " + std::to_string(v[0]) + ")")
+                  : fail(TQ_ERR_DEVICE_INPUT, "a libtq kernel met a position, slot, page or length out of range");
   }
   return TQ_OK;
 }

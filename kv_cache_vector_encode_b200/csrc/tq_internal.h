@@ -44,11 +44,13 @@ constexpr float kSplitScaleInv = 1.0f / 4096.0f;
 
 bool valid_dim(int d);       // multiple of 32 in [32, 4096]
 
-// Code of an index in device data (position, slot, page, length) out of its range, next to sm100.cuh's DeviceError.
-constexpr uint32_t kDevBadInput = 16;
-
-// Device address of the library's error word (kernels record bounded-wait timeouts and bad indices there).
+// Device address of the library's error words: [0] the first bounded-wait timeout (sm100.cuh's DeviceError), [1] non-zero
+// once a kernel has met an index in device data (position, slot, page, length) out of its range. A word each, so that
+// neither hides the other.
 uint32_t* device_error_word();
+#ifdef __CUDACC__
+__device__ __forceinline__ void report_bad_input(uint32_t* err) { atomicExch(err + 1, 1u); }
+#endif
 
 // Number of SMs of the current device.
 int sm_count();
