@@ -416,9 +416,10 @@ TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, 
  *   scale       0 (or any value that is not > 0) selects 1/sqrt(d)
  *   out         [total_q][Hq][d] TQ_BF16, contiguous
  * Lengths or page numbers outside their ranges are reported by tq_sync_check (TQ_ERR_DEVICE_INPUT): a bad page's
- * tokens, and those past max_kv_len or max_pages, are taken as not seen; a sequence with a bad q_start has no
- * queries, and its outputs are left as they were. A record with a norm that is not finite makes the rows that see
- * it not finite, and no others, and so does a query vector that is not finite its own row (under a softcap too).
+ * tokens, and those past max_kv_len or max_pages, are taken as not seen (the queries stand where kv_len says; a
+ * negative length counts as 0); a sequence with a bad q_start has no queries, and its outputs are left as they were. A
+ * record with a norm that is not finite makes the rows that see it not finite, and no others, and so does a query
+ * vector that is not finite its own row (under a softcap too).
  * Softmax and sums in fp32. A sequence with few query rows per KV head (Qn Hq / Hkv up to 48, up to 256 where B Hkv is small) meets the codes
  * themselves: its queries and the key levels enter the tensor cores as 16-bit integers, value levels and softmax
  * weights as fp16. A longer chunk's visible tokens are decoded once into fp16 tiles in the workspace, by groups of

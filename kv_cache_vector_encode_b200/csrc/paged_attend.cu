@@ -367,7 +367,6 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   if (((uintptr_t)q_start | (uintptr_t)kv_len | (uintptr_t)page_table | (uintptr_t)prefix_len | (uintptr_t)slopes) & 3)
     return fail(TQ_ERR_INVALID_ARG, f + ": int32 / fp32 arrays must be 4-byte aligned");
   if (!work) return TQ_OK;
-  if (window >= max_kv_len) window = 0;
   const int g = Hq / kv->Hkv;
   const Plan P = plan(kv, B, Hq, total_q, max_q_len, max_kv_len, prefix_len ? 0 : window);
   if (!ws || ws_bytes < tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len))

@@ -49,10 +49,11 @@ struct PagedAttendParams {
   uint32_t* err;
 };
 
-// One sequence of the call, its lengths checked against the limits the launch was sized for.
+// One sequence of the call, its lengths checked against the limits the launch was sized for. Past the limits (an error
+// that is reported) no token is seen, but the queries stand where kv says.
 struct PagedSeq {
   int q0, qn;                  // first query row, number of queries
-  int64_t kv;                  // filled slots
+  int64_t kv, end;             // filled slots; those that may be read
 };
 
 // The chunk kernels (paged_chunk.cu): their share of the workspace, and the launch.
@@ -101,19 +102,17 @@ __device__ __forceinline__ PagedSeq paged_seq_checked(const PagedAttendParams& p
   PagedSeq s;
   s.q0 = p.q_start[b];
   int q1 = p.q_start[b + 1];
-  int64_t kv = p.kv_len[b];
+  const int64_t kv = p.kv_len[b];
   const int64_t most = min(p.max_kv, (int64_t)p.max_pages << p.page_shift);
   bad = false;
   if (s.q0 < 0 || q1 < s.q0 || q1 > p.total_q || q1 - s.q0 > p.max_q) {
     bad = true;
     s.q0 = q1 = 0;
   }
-  if (kv < 0 || kv > most) {
-    bad = true;
-    kv = kv < 0 ? 0 : most;
-  }
+  if (kv < 0 || kv > most) bad = true;
   s.qn = q1 - s.q0;
-  s.kv = kv;
+  s.kv = max(kv, (int64_t)0);
+  s.end = min(s.kv, most);
   return s;
 }
 __device__ __forceinline__ PagedSeq paged_seq_quiet(const PagedAttendParams& p, int b) {
@@ -130,7 +129,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b)
 // Tokens [lo, hi) that the queries at positions [p0, p1] of a sequence may see between them.
 __device__ __forceinline__ void paged_range(const PagedAttendParams& p, const PagedSeq& s, int64_t p0, int64_t p1,
                                             int64_t prefix, int64_t& lo, int64_t& hi) {
-  hi = min(s.kv, max(p1 + 1, prefix));
+  hi = min(s.end, max(p1 + 1, prefix));
   lo = p.window > 0 && prefix <= 0 ? max((int64_t)0, p0 - p.window + 1) : 0;
   if (hi < lo) hi = lo;
 }

@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int w = 0; w < kHalf / 32; ++w) {
           // seen: present and ((t <= pos and t > pos - window) or t < prefix)
           const int at = t0 + 32 * w;
-          uint32_t m = below(pos + 1 - at);
+          uint32_t m = below(min(pos - at, 31) + 1);             // pos may be 2^31 - 1
           if (p.window > 0) m &= ~below(pos - p.window + 1 - at);
           m |= below(pre - at);
           m = on ? m & __ldg(&head->present[2 * half + w]) : 0u;

@@ -133,8 +133,9 @@ __device__ __forceinline__ int row_blocks_of(const PagedAttendParams& p, const P
   const int64_t first = s.kv - s.qn;
   const int j0 = row0 == 0 ? 0 : row0 / p.g, j1 = row0 + p.rows_per_item >= rows ? s.qn - 1 : (row0 + p.rows_per_item - 1) / p.g;
   paged_range(p, s, first + j0, first + j1, prefix, lo, hi);
+  if (hi <= lo) return 0;      // before lo moves to the start of its block
   lo &= ~15LL;
-  return hi > lo ? (int)((hi - lo + 15) >> 4) : 0;
+  return (int)((hi - lo + 15) >> 4);
 }
 
 // Where a CTA starts. Its range counts blocks of all items, or (unit > 0) parts of all items, of `unit` blocks at most.

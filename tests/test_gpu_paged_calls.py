@@ -1,6 +1,10 @@
 """The paged operators' calls at the edges of what their documentation allows (B200)."""
+
+import numpy as np
 import pytest
 
+from test_gpu_paged import Paged, queries
+from test_gpu_paged_formats import check
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +39,26 @@ def test_bad_input_does_not_hide_a_timeout(dev, input_first):
     for call in todo if input_first else todo[::-1]:
         call()
     assert [status_of_check() for _ in range(3)] == [tq.TQ_ERR_DEVICE_TIMEOUT, tq.TQ_ERR_DEVICE_INPUT, tq.TQ_OK]
+
+
+# ---- lengths past the limits ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("by_pages", [False, True])
+@pytest.mark.parametrize("opt", [{}, dict(window=70), dict(window=240), dict(slopes=True), dict(prefix=[20, 9, 0])])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [9, 2, 1], [140, 70, 1]])
+def test_attend_lengths_past_the_limits(dev, q_lens, opt, by_pages):
+    """A length above max_kv_len, or above what max_pages hold, is reported; the tokens behind the limit are not seen,
+    and the queries stand where the length says."""
+    lens, Hq, Hkv, d, ps, most = [300, 200, 90], 4, 2, 64, 16, 240
+    pool = Paged(dev, lens, Hkv, d, 3, 3, 1, ps, seed=5)
+    q = queries(np.random.default_rng(3), sum(q_lens), Hq, d, dev)
+    opt = dict(opt)
+    if opt.pop("slopes", False):
+        opt["slopes"] = (2.0 ** (-4.0 * np.arange(1, Hq + 1) / Hq)).astype(np.float32)
+    whole = pool.table
+    if by_pages:
+        pool.table = np.ascontiguousarray(whole[:, : most // ps])
+    out = pool.call(q, q_lens, max_kv=max(lens) if by_pages else most, **opt)
+    assert status_of_check() == tq.TQ_ERR_DEVICE_INPUT
+    pool.table = whole
+    check(pool, out, q, q_lens, present=[np.arange(300) < most, None, None], **opt)
