@@ -855,6 +855,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (ok) {
       tc_fence_after();
       if (n > 0 && !(fine && fabsf(slope) < INFINITY)) sum = __int_as_float(0x7FC00000);   // the cap and the polynomial may have hidden it
+      // a query before the first token sees nothing, whatever it holds (the polynomial's weights are not quite 0 there)
+      if (pos < 0 && pre <= 0) sum = 0.f;
       const float inv = sum == 0.f ? 0.f : __int_as_float((127 - kBits) << 23) / sum;
       uint4* dst = (uint4*)(p.out + ((int64_t)(x.sq.q0 + jq) * p.Hq + h) * D);
 #pragma unroll

@@ -62,3 +62,23 @@ def test_attend_lengths_past_the_limits(dev, q_lens, opt, by_pages):
     assert status_of_check() == tq.TQ_ERR_DEVICE_INPUT
     pool.table = whole
     check(pool, out, q, q_lens, present=[np.arange(300) < most, None, None], **opt)
+
+
+# ---- rows that see nothing -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("lens,q_lens", [([20, 40], [150, 90]), ([3, 1], [9, 2])])
+def test_attend_rows_that_see_nothing(dev, lens, q_lens, softcap):
+    """More queries than tokens (a batch padded at its front): the first rows see nothing and are 0, whatever stands in
+    their queries, in chunks as in steps."""
+    Hq, Hkv, d = 4, 1, 128
+    pool = Paged(dev, lens, Hkv, d, 3, 3, 2, 16, seed=7)
+    q = queries(np.random.default_rng(7), sum(q_lens), Hq, d, dev)
+    start = np.concatenate([[0], np.cumsum(q_lens)])
+    for what in (float("nan"), float("inf"), 3e38):
+        bad = q.clone()
+        for b, (n, m) in enumerate(zip(lens, q_lens)):
+            bad[start[b]:start[b] + max(m - n, 0)] = what
+        out = pool.call(bad, q_lens, softcap=softcap)
+        tq.tq_sync_check()
+        check(pool, out, q, q_lens, softcap=softcap)
