@@ -411,7 +411,7 @@ TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, 
  *               outputs left as they were
  *   kv_len      [B] int32;  page_table [B][max_pages] int32, read up to page (kv_len[b] - 1) / page_size
  *   max_q_len, max_kv_len  at least the longest Qn and kv_len (they size the launch and the workspace)
- *   prefix_len  [B] int32 or NULL: tokens before it are seen by every query
+ *   prefix_len  [B] int32 or NULL: tokens before it are seen by every query (none where it is not positive)
  *   slopes      [Hq] fp32 or NULL
  *   scale       0 (or any value that is not > 0) selects 1/sqrt(d)
  *   out         [total_q][Hq][d] TQ_BF16, contiguous

@@ -126,6 +126,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b)
   return s;
 }
 
+// Tokens of a sequence that every query sees (a negative prefix is none).
+__device__ __forceinline__ int64_t paged_prefix(const PagedAttendParams& p, const PagedSeq& s, int b) {
+  return p.prefix ? max((int64_t)0, min((int64_t)p.prefix[b], s.kv)) : 0;
+}
+
 // Tokens [lo, hi) that the queries at positions [p0, p1] of a sequence may see between them.
 __device__ __forceinline__ void paged_range(const PagedAttendParams& p, const PagedSeq& s, int64_t p0, int64_t p1,
                                             int64_t prefix, int64_t& lo, int64_t& hi) {

@@ -105,7 +105,7 @@ __device__ __forceinline__ bool find_unit(const PagedAttendParams& p, const Chun
   x.b = c.list[1 + slot];
   x.sq = paged_seq(p, x.b);
   x.first = x.sq.kv - x.sq.qn;
-  x.prefix = p.prefix ? min((int64_t)p.prefix[x.b], x.sq.kv) : 0;
+  x.prefix = paged_prefix(p, x.sq, x.b);
   paged_range(p, x.sq, x.first, x.first + x.sq.qn - 1, x.prefix, x.lo, x.hi);
   return true;
 }

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
   {
     auto count = [&](int b, int unit) {
       const PagedSeq s = paged_seq_quiet(p, b);
-      const int64_t prefix = p.prefix ? min((int64_t)p.prefix[b], s.kv) : 0;
+      const int64_t prefix = paged_prefix(p, s, b);
       int64_t lo, hi, n = 0;
       for (int rb = 0; rb < p.row_blocks; ++rb) n += row_parts(row_blocks_of(p, s, prefix, rb, lo, hi), unit);
       return n * p.Hkv;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
   for (int b = start.b; pos < start.end && b < p.B; ++b) {
     const PagedSeq sq = paged_seq(p, b);
     const int64_t first = sq.kv - sq.qn;                         // position of query 0
-    const int64_t prefix = p.prefix ? min((int64_t)p.prefix[b], sq.kv) : 0;
+    const int64_t prefix = paged_prefix(p, sq, b);
     const int rows = sq.qn * p.g;
     // items in the order of their numbers, so that (CTA + item) grows with every part
     int hkv = 0;

@@ -82,3 +82,18 @@ def test_attend_rows_that_see_nothing(dev, lens, q_lens, softcap):
         out = pool.call(bad, q_lens, softcap=softcap)
         tq.tq_sync_check()
         check(pool, out, q, q_lens, softcap=softcap)
+
+
+# ---- prefixes out of range -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [0, 31])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [140, 130, 2]])
+def test_attend_prefixes_out_of_range(dev, q_lens, window):
+    """A negative prefix, down to the type's lowest value, is none; one past the sequence is all of it."""
+    lens, Hq, Hkv, d = [300, 200, 90], 4, 2, 128
+    pool = Paged(dev, lens, Hkv, d, 3, 3, 2, 16, seed=15)
+    q = queries(np.random.default_rng(15), sum(q_lens), Hq, d, dev)
+    for prefix in ([-2**31, -1, 2**31 - 1], [2**31 - 1, -2**31, -2**31 + 100], [-2**31 + 5, 2**31 - 1, 0]):
+        out = pool.call(q, q_lens, prefix=prefix, window=window)
+        tq.tq_sync_check()
+        check(pool, out, q, q_lens, prefix=prefix, window=window)
