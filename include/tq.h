@@ -376,7 +376,8 @@ TQ_API tq_status tq_paged_kv_init(const tq_codebook* cb_k, const tq_codebook* cb
 /* Appends the keys and values of `tokens` new tokens: token t's records go to slot slots[t] of every
  * KV head, the key turned to positions[t] on the way (tq_rope's formula, without rounding the turned
  * key). A record equals tq_encode_mse / tq_encode_prod of the (turned) vector, with every index and sign
- * decided as in fp64. Norms are those of the (turned) vector; residual norms are taken from an fp32 residual.
+ * decided as in fp64, whatever the length of the rows of S. Norms are those of the (turned) vector;
+ * residual norms are taken from an fp32 residual.
  *   k_new, v_new  [tokens][Hkv][d] in x_dtype (TQ_F32 or TQ_BF16); token t at t * k_token_stride
  *                 (v_token_stride) elements, heads d apart; rows 16-byte aligned
  *   slots         [tokens] int64; a negative slot marks a row that only pads the batch: nothing of it is

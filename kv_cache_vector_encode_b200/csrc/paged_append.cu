@@ -45,6 +45,7 @@ struct AppendParams {
   const float* Pi;
   const float* S;
   const float* T;              // S Pi^T
+  const float* s_len;          // length of the longest row of S
   const uint8_t* img[4];       // shared-memory images of the rows of Pi and S: high and low parts of each
   uint32_t* k_codes;
   uint16_t* k_norms;
@@ -64,8 +65,22 @@ constexpr int kVec = 128;              // vectors of a tile
 constexpr float kBandY = 3.8146973e-6f;   // 2^-18
 // the length itself is rounded to fp16 only where 2^-20 of it makes no difference
 constexpr float kBandN = 9.5367432e-7f;   // 2^-20
-// s = S r takes the error of r times up to |S_i|; decided again by |s| < band
-constexpr float kBandS = 1.2207031e-4f;   // 2^-13
+// A sign is decided again where |s| < band, s = (S r)_i. As vectors over the coordinates, with |u| = 1, |c| <= 1 + gamma:
+//   Pi^T c   for the splits 2^-22 sqrt(D) |c| twice (Pi's low part rounded, low times low left out: elementwise 2^-22 of
+//            Pi, whose Frobenius norm is sqrt(D)) and 2^-22 |c| (c's low part rounded: Pi keeps its length). The accumulation
+//            is taken to lose up to two units of the largest of a step's sums and products, 2^-22 of it. Sums of the first k
+//            steps have length |c_1..k| <= |c|, products of a step |c_step|: 2^-22 (sqrt(2) K + sqrt(K)) |c| over K = D / 16
+//            steps. And 2^-22 |c| where the parts meet in fp32
+//   u        2^-21.3 for the length
+//   S r      (3 + K) 2^-22 |S_i| gamma for the product itself, everything above times |S_i|
+// so band = max |S_i| ((1 + gamma) kBandC + gamma kBandP + 2^-21), 1.8e-4 at D = 128, |S_i| = 13, gamma = 0.35.
+template <int D> struct SignBand {
+  static constexpr float kSteps = D / 16, kRoot = D == 128 ? 11.313708f : 8.f, kStepRoot = D == 128 ? 2.8284271f : 2.f, kUnit = 2.3841858e-7f;
+  static constexpr float kBandC = (2.f * kRoot + 1.4142136f * kSteps + kStepRoot + 2.f) * kUnit, kBandP = (3.f + kSteps) * kUnit;
+  static __device__ __forceinline__ float of(float s_len, float gamma) {
+    return s_len * fmaf(gamma, kBandC + kBandP, kBandC + 2.f * kUnit);
+  }
+};
 constexpr float kResScale = 8192.f;    // 2^13: |r| < 4 keeps fp16 in range
 
 template <int D>
@@ -518,8 +533,13 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
       split8(w, smem + L::kOpHi + off, smem + L::kOpLo + off);
     }
     part[g * kVec + v] = gs;
+    const float s_len = __ldg(p.s_len);                          // before the wait
     if (!product(L::kSHi, false)) break;
     // ---- signs -------------------------------------------------------------------------------------------------
+    gs = 0.f;
+#pragma unroll
+    for (int k = 0; k < G; ++k) gs += part[k * kVec + v];
+    const float gamma = sqrtf(gs), band = SignBand<D>::of(s_len, gamma) * kResScale;
     uint32_t sign = 0;
     near = 0;
 #pragma unroll
@@ -532,7 +552,7 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
       for (int k = 0; k < 16; ++k) {
         const float s = fmaf(__uint_as_float(b[k]), kSplitScaleInv, __uint_as_float(a[k]));
         sign |= (uint32_t)(s >= 0.f) << (c + k);
-        near |= (uint32_t)(fabsf(s) < kBandS * kResScale) << (c + k);
+        near |= (uint32_t)(fabsf(s) < band) << (c + k);
       }
     }
     if (!ok) near = 0;                                           // r is exactly zero
@@ -580,12 +600,7 @@ __global__ void __launch_bounds__(4 * D, 1) append_kernel(const __grid_constant_
     }
     if (rec >= 0) {
       p.v_signs[rec * G + g] = sign;
-      if (g == 0) {
-        gs = 0.f;
-#pragma unroll
-        for (int k = 0; k < G; ++k) gs += part[k * kVec + v];
-        p.v_gammas[rec] = __half_as_ushort(__float2half_rn(sqrtf(gs)));
-      }
+      if (g == 0) p.v_gammas[rec] = __half_as_ushort(__float2half_rn(gamma));
     }
     tc_fence_before();
     __syncthreads();
@@ -644,6 +659,7 @@ extern "C" TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t token
   p.Pi = (const float*)((const uint8_t*)rot + RL.pi32);
   p.S = (const float*)((const uint8_t*)rot + RL.s32);
   p.T = (const float*)((const uint8_t*)rot + RL.t32);
+  p.s_len = (const float*)((const uint8_t*)rot + kRotSLen);
   const size_t img[4] = {RL.pi_hi, RL.pi_lo, RL.s_hi, RL.s_lo};
   for (int i = 0; i < 4; ++i) p.img[i] = (const uint8_t*)rot + img[i];
   p.k_codes = kv->k_codes;

@@ -89,9 +89,20 @@ __global__ void split_kernel(const float* __restrict__ M, int d, int dp, bool tr
   lo[off / 2] = l;
 }
 
-__global__ void header_kernel(int* hdr, int d) {
+// One block of 128; thread = row of S, whose longest row is told for d <= 128 alone (the paged append's d).
+__global__ void __launch_bounds__(128) header_kernel(int* hdr, int d, const float* __restrict__ S) {
+  __shared__ double length2[128];
+  double n = 0.0;
+  if (d <= 128 && (int)threadIdx.x < d)
+    for (int j = 0; j < d; ++j) n = fma((double)S[threadIdx.x * d + j], (double)S[threadIdx.x * d + j], n);
+  length2[threadIdx.x] = n;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  double most = 0.0;
+  for (int i = 0; i < 128; ++i) most = fmax(most, length2[i]);
   hdr[0] = 0x54515231;  // "TQR1"
   hdr[1] = d;
+  ((float*)hdr)[kRotSLen / 4] = __double2float_ru(sqrt(most));
 }
 
 }  // namespace
@@ -161,7 +172,7 @@ extern "C" TQ_API tq_status tq_rotation_prepare(int32_t d, const float* Pi, cons
   split_kernel<<<blocks, 256, 0, st>>>(S, d, L.dp, true, (__half*)(base + L.st_hi), (__half*)(base + L.st_lo));
   if (d <= 128)
     split_kernel<<<blocks, 256, 0, st>>>(S, d, L.dp, false, (__half*)(base + L.s_hi), (__half*)(base + L.s_lo));
-  header_kernel<<<1, 1, 0, st>>>((int*)base, d);
+  header_kernel<<<1, 128, 0, st>>>((int*)base, d, S);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "tq_rotation_prepare: launch");
   return TQ_OK;
 }

@@ -38,6 +38,9 @@ struct RotLayout {
   size_t total;
 };
 RotLayout rot_layout(int d);
+// The header (256 bytes) holds a magic number, d and, at this byte, the length of the longest row of S (fp32, rounded
+// up; 0 for d > 128).
+constexpr size_t kRotSLen = 8;
 
 constexpr float kSplitScale = 4096.0f;      // 2^12: scale of the low fp16 part of a split
 constexpr float kSplitScaleInv = 1.0f / 4096.0f;

@@ -3,7 +3,11 @@
 import numpy as np
 import pytest
 
-from test_gpu_paged import Paged, queries
+import workloads as W
+from oracle import quant as Q
+from oracle.codebook import lloyd_max
+from parity import np_u32
+from test_gpu_paged import Paged, filled, queries, rotation
 from test_gpu_paged_formats import check
 
 pytestmark = pytest.mark.gpu
@@ -97,3 +101,35 @@ def test_attend_prefixes_out_of_range(dev, q_lens, window):
         out = pool.call(q, q_lens, prefix=prefix, window=window)
         tq.tq_sync_check()
         check(pool, out, q, q_lens, prefix=prefix, window=window)
+
+
+# ---- signs next to zero --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("log2_length", [0, 12])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_signs_next_to_zero(dev, d, log2_length):
+    """Signs as in fp64, of vectors made so that one coordinate of S r vanishes but for the rounding of the vector to
+    fp32, and whatever the length of S's rows (which changes no sign)."""
+    Hkv, tokens, ps = 4, 2048, 64
+    n = tokens * Hkv
+    Pi, S = W.rotation(d), W.jl_matrix(d) * np.float32(2.0**log2_length)
+    cb = lloyd_max(d, 2)
+    rng = np.random.default_rng(d)
+    x = rng.standard_normal((n, d))
+    at = np.arange(n) % d
+    for _ in range(5):                                           # the indices may move with x: again
+        s = Q.encode_prod(x, Pi, S, cb)["s"][np.arange(n), at]
+        row = S[at].astype(np.float64)
+        x -= row * (s * np.linalg.norm(x, axis=1) / (row**2).sum(1))[:, None]
+    x = x.astype(np.float32)
+    e = Q.encode_prod(x.astype(np.float64), Pi, S, cb)
+    close = np.abs(e["s"][np.arange(n), at]) < 1e-6 * 2.0**log2_length
+    assert close.mean() > 0.3
+    rot = tq.tq_rotation_prepare(torch.from_numpy(Pi).to(dev), torch.from_numpy(S).to(dev))
+    kv = filled(dev, tokens // ps, Hkv, ps, d, 1, 3, 2)
+    v = torch.from_numpy(x.reshape(tokens, Hkv, d)).to(dev)
+    tq.tq_paged_append(kv, v, v, torch.arange(tokens, device=dev), rot)
+    tq.tq_sync_check()
+    got = Q.unpack_signs(np_u32(kv.tensors[4]).swapaxes(1, 2).reshape(n, d // 32))
+    wrong = (got != e["z"]) & (np.abs(e["s"]) >= 1e-11 * 2.0**log2_length)
+    assert not wrong.any(), int(wrong.sum())
