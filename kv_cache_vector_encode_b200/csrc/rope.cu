@@ -227,13 +227,16 @@ extern "C" TQ_API tq_status tq_rope(int64_t tokens, int32_t heads, int32_t d, in
   if ((uintptr_t)x % es || (uintptr_t)out % es || (uintptr_t)positions % 4 || (uintptr_t)table % 8)
     return fail(TQ_ERR_INVALID_ARG, f + ": pointers must be aligned to their elements (table to 8 bytes)");
   if (x_token_stride < 0 || x_head_stride < 0) return fail(TQ_ERR_INVALID_ARG, f + ": negative stride");
-  // every output element has one writer: heads must not overlap within a token, nor tokens each other
-  auto apart = [](int64_t inner, int64_t n, int64_t outer, int64_t len) { return inner >= len && outer >= inner * (n - 1) + len; };
+  // every output element has one writer: heads must not overlap within a token, nor tokens each other. The stride of an
+  // axis of length one has no meaning
+  auto apart = [](int64_t inner, int64_t n, int64_t outer, int64_t len) {
+    return inner >= len && outer >= (__int128)inner * (n - 1) + len;
+  };
   const int64_t ot = tokens > 1 ? out_token_stride : INT64_MAX, oh = heads > 1 ? out_head_stride : INT64_MAX;
-  if (out_head_stride < 0 || out_token_stride < 0 || out_head_stride > INT32_MAX || tokens > INT32_MAX ||
+  if (out_head_stride < 0 || out_token_stride < 0 ||
       !(ot < oh ? apart(ot, tokens, oh, d) : (oh == INT64_MAX || apart(oh, heads, ot, d))))
     return fail(TQ_ERR_INVALID_ARG, f + ": output strides must keep heads and tokens apart");
-  if (x == out && tokens > 0 && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+  if (x == out && ((tokens > 1 && x_token_stride != out_token_stride) || (heads > 1 && x_head_stride != out_head_stride)))
     return fail(TQ_ERR_INVALID_ARG, f + ": in place needs the same strides");
   if (tokens == 0) return TQ_OK;
   if (tokens > ((int64_t)1 << 31) - 1 || heads > (1 << 20)) return fail(TQ_ERR_UNSUPPORTED, f + ": tokens or heads too many");

@@ -7,7 +7,7 @@ import workloads as W
 from oracle import quant as Q
 from oracle.codebook import lloyd_max
 from parity import np_u32
-from test_gpu_paged import Paged, filled, queries, rotation
+from test_gpu_paged import Paged, filled, i32, queries, rotation
 from test_gpu_paged_formats import check
 
 pytestmark = pytest.mark.gpu
@@ -101,6 +101,34 @@ def test_attend_prefixes_out_of_range(dev, q_lens, window):
         out = pool.call(q, q_lens, prefix=prefix, window=window)
         tq.tq_sync_check()
         check(pool, out, q, q_lens, prefix=prefix, window=window)
+
+
+# ---- strides --------------------------------------------------------------------------
+
+def test_rope_head_strides_past_32_bits(dev):
+    """Heads outermost, further apart than 2^31 elements, in place and out of place."""
+    far, tokens, d = (1 << 31) + 64, 3, 64
+    rng = np.random.default_rng(1)
+    buf = torch.empty(far + tokens * d, dtype=torch.bfloat16, device=dev)
+    x = buf.as_strided((tokens, 2, d), (d, far, 1))
+    x.copy_(torch.from_numpy(rng.standard_normal((tokens, 2, d))).to(dev))
+    table, pos = tq.tq_rope_table(50, d), i32([7, 0, 49], dev)
+    near = x.clone()
+    tq.tq_rope(near, pos, table)
+    out = torch.empty_like(near)
+    tq.tq_rope(x, pos, table, out=out)
+    assert torch.equal(out, near)
+    tq.tq_rope(x, pos, table)
+    assert torch.equal(x, near)
+
+
+def test_rope_in_place_through_another_view(dev):
+    """The stride of an axis of length one has no meaning."""
+    table, pos = tq.tq_rope_table(50, 64), i32([7], dev)
+    x = torch.randn(1, 4, 64, device=dev)
+    want = tq.tq_rope(x.clone(), pos, table)
+    tq.tq_rope(x, pos, table, out=x.as_strided((1, 4, 64), (64, 64, 1)))
+    assert torch.equal(x, want)
 
 
 # ---- signs next to zero --------------------------------------------------------------------------
