@@ -471,6 +471,14 @@ def _in(t, name, device, dtype, *shape):
     return t.data_ptr()
 
 
+def _fits(*values, bits=32):
+    """The integers that a caller gives have to fit their C types, which would cut them short."""
+    most = 1 << (bits - 1)
+    for v in values:
+        if not -most <= v < most:
+            raise ValueError(f"{v} does not fit {bits} bits")
+
+
 def _table(table, device):
     """Address, positions and rotated dimensions of a tq_rope_table."""
     if table.get_device() != device or table.dtype is not _tc.f32 or table.dim() != 3 or not table.is_contiguous():
@@ -492,6 +500,7 @@ def tq_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: int 
                   magnitude: float = 1.0, device="cuda", stream=None):
     """Table [n_pos, rot_dim // 2, 2] float32 of (cos, sin) for tq_rope and tq_paged_append."""
     import torch
+    _fits(rot_dim, scaling)
     device = torch.device(device)
     table = _empty((n_pos, rot_dim // 2, 2), torch.float32, device, stream, keep=True)
     _current(table, "device")
@@ -520,6 +529,7 @@ def tq_rope(x, positions, table, out=None, layout: int = TQ_ROPE_HALF, inverse: 
         raise ValueError("the last axis of x and out must be contiguous")
     pos = _in(positions, "positions", device, _tc.i32, tokens)
     tab, n_pos, rot_dim = _table(table, device)
+    _fits(layout)
     status = _lib.tq_rope(tokens, heads, d, rot_dim, layout, 1 if inverse else 0, x.data_ptr(), xt, xh, code, pos, tab, n_pos,
                           out.data_ptr(), os_[0], os_[1], _raw(stream, device))
     if status:
@@ -583,6 +593,7 @@ def tq_paged_append(kv: PagedKV, k_new, v_new, slots, rot, positions=None, table
         tab, n_pos, rot_dim = _table(table, device)
     elif positions is not None or table is not None:
         raise ValueError("positions and table go together")
+    _fits(layout)
     status = _lib.tq_paged_append(kv.ref, tokens, k_new.data_ptr(), strides[0], v_new.data_ptr(), strides[1], _tc.code[dtype],
                                   at, pos, tab, n_pos, rot_dim, layout, _prepared(rot, kv), _raw(stream, device))
     if status:
@@ -597,6 +608,8 @@ def _prepared(rot, kv):
 
 
 def tq_paged_attend_workspace_bytes(kv: PagedKV, B: int, Hq: int, total_q: int, max_q_len: int, max_kv_len: int) -> int:
+    _fits(B, Hq, max_q_len)
+    _fits(total_q, max_kv_len, bits=64)
     return int(lib().tq_paged_attend_workspace_bytes(kv.ref, B, Hq, total_q, max_q_len, max_kv_len))
 
 
@@ -623,8 +636,9 @@ def tq_paged_attend(kv: PagedKV, q, q_start, kv_len, page_table, rot, out, max_q
     pages = _in(page_table, "page_table", device, i32, B, max_pages)
     prefix = None if prefix_len is None else _in(prefix_len, "prefix_len", device, i32, B)
     slope = None if slopes is None else _in(slopes, "slopes", device, _tc.f32, Hq)
+    _fits(max_q_len, window)
+    _fits(max_kv_len, bits=64)
     if ws is None:
-        import torch
         ws = _empty(max(tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len), 16), torch.uint8,
                     q.device, stream)
     elif ws.get_device() != device or not ws.is_contiguous():

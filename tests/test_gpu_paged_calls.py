@@ -131,6 +131,25 @@ def test_rope_in_place_through_another_view(dev):
     assert torch.equal(x, want)
 
 
+# ---- ranges of the arguments ---------------------------------------------------------------------
+
+def test_arguments_past_32_bits_are_refused(dev):
+    """A window or a length that does not fit the C type is not cut to one that does."""
+    pool = Paged(dev, [40], 1, 64, 3, 3, 1, 16, seed=1)
+    q = queries(np.random.default_rng(1), 1, 1, 64, dev)
+    for bad in (dict(window=(1 << 32) + 5), dict(window=-(1 << 32) + 5), dict(max_q=(1 << 32) + 1), dict(max_kv=(1 << 64) + 40)):
+        with pytest.raises((ValueError, tq.TQError)):
+            pool.call(q, [1], **bad)
+    with pytest.raises((ValueError, tq.TQError)):
+        tq.tq_paged_attend_workspace_bytes(pool.kv, 1, 1, 1, (1 << 32) + 1, 40)
+    x = torch.ones(1, 1, 64, device=dev)
+    with pytest.raises((ValueError, tq.TQError)):
+        tq.tq_rope(x, i32([1], dev), tq.tq_rope_table(4, 64), layout=1 << 32)
+    with pytest.raises((ValueError, tq.TQError)):
+        tq.tq_paged_append(pool.kv, x, x, torch.zeros(1, dtype=torch.int64, device=dev), rotation(64, dev)[2], layout=1 << 32)
+    tq.tq_sync_check()
+
+
 # ---- signs next to zero --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("log2_length", [0, 12])
