@@ -639,7 +639,7 @@ def tq_paged_attend(kv: PagedKV, q, q_start, kv_len, page_table, rot, out, max_q
     _fits(max_q_len, window)
     _fits(max_kv_len, bits=64)
     if ws is None:
-        ws = _empty(max(tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len), 16), torch.uint8,
+        ws = _empty(max(tq_paged_attend_workspace_bytes(kv, B, Hq, total_q, max_q_len, max_kv_len), 16), _tc.u8,
                     q.device, stream)
     elif ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous and on device {device}")
