@@ -403,7 +403,7 @@ TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, 
  * t % page_size; its Qn = q_start[b+1] - q_start[b] newest tokens are the queries q_start[b] .. of q, query j
  * at position pos = kv_len[b] - Qn + j:
  *   x_t   = scale <q[j][h], k_hat_t>                        (k_hat, v_hat: the decoded records)
- *   x_t   = softcap tanh(x_t / softcap)                     (softcap >= 1e-30; 0: no cap)
+ *   x_t   = softcap tanh(x_t / softcap)                     (softcap >= 1e-30; 0, or 2^100 and above: no cap)
  *   x_t  += slopes[h] (t - pos)                             (slopes given: a bias by distance)
  *   seen:   t < kv_len[b] and ((t <= pos and (window = 0 or t > pos - window)) or t < prefix_len[b])
  *   out[j][h] = sum over seen t of softmax_t(x) v_hat_t;    0 where nothing is seen

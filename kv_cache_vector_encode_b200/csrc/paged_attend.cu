@@ -400,6 +400,7 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   p.out = (uint16_t*)out;
   p.scale_log2 = scale * kLog2e;
   p.key_fac = p.scale_log2 * 256.0f / limb_table(kv->ck, kv->k_bits, p.klimb);
+  if (softcap >= 1.2676506e30f) softcap = 0.0f;   // 2^100: it would change no score below 2^88 by as much as a rounding
   p.cap_log2 = softcap * kLog2e;
   p.cap2x = softcap > 0.0f ? 2.0f / softcap : 0.0f;   // x arrives times log2(e), as exp2 wants it
   p.v_inv_unit = 1.0f / kv->v_unit;

@@ -50,10 +50,10 @@ struct PagedAttendParams {
 };
 
 // One sequence of the call, its lengths checked against the limits the launch was sized for. Past the limits (an error
-// that is reported) no token is seen, but the queries stand where kv says.
+// that is reported) no token is seen, but the queries stand where the length says.
 struct PagedSeq {
   int q0, qn;                  // first query row, number of queries
-  int64_t kv, end;             // filled slots; those that may be read
+  int first, end;              // position of query 0 (filled slots less queries); slots that may be read
 };
 
 // The chunk kernels (paged_chunk.cu): their share of the workspace, and the launch.
@@ -102,8 +102,7 @@ __device__ __forceinline__ PagedSeq paged_seq_checked(const PagedAttendParams& p
   PagedSeq s;
   s.q0 = p.q_start[b];
   int q1 = p.q_start[b + 1];
-  const int64_t kv = p.kv_len[b];
-  const int64_t most = min(p.max_kv, (int64_t)p.max_pages << p.page_shift);
+  const int kv = p.kv_len[b], most = (int)min(p.max_kv, (int64_t)p.max_pages << p.page_shift);
   bad = false;
   if (s.q0 < 0 || q1 < s.q0 || q1 > p.total_q || q1 - s.q0 > p.max_q) {
     bad = true;
@@ -111,8 +110,8 @@ __device__ __forceinline__ PagedSeq paged_seq_checked(const PagedAttendParams& p
   }
   if (kv < 0 || kv > most) bad = true;
   s.qn = q1 - s.q0;
-  s.kv = max(kv, (int64_t)0);
-  s.end = min(s.kv, most);
+  s.first = max(kv, 0) - s.qn;
+  s.end = max(0, min(kv, most));
   return s;
 }
 __device__ __forceinline__ PagedSeq paged_seq_quiet(const PagedAttendParams& p, int b) {
@@ -128,13 +127,13 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttendParams& p, int b)
 
 // Tokens of a sequence that every query sees (a negative prefix is none).
 __device__ __forceinline__ int64_t paged_prefix(const PagedAttendParams& p, const PagedSeq& s, int b) {
-  return p.prefix ? max((int64_t)0, min((int64_t)p.prefix[b], s.kv)) : 0;
+  return p.prefix ? max(0, min(p.prefix[b], s.end)) : 0;
 }
 
 // Tokens [lo, hi) that the queries at positions [p0, p1] of a sequence may see between them.
 __device__ __forceinline__ void paged_range(const PagedAttendParams& p, const PagedSeq& s, int64_t p0, int64_t p1,
                                             int64_t prefix, int64_t& lo, int64_t& hi) {
-  hi = min(s.end, max(p1 + 1, prefix));
+  hi = min((int64_t)s.end, max(p1 + 1, prefix));
   lo = p.window > 0 && prefix <= 0 ? max((int64_t)0, p0 - p.window + 1) : 0;
   if (hi < lo) hi = lo;
 }
@@ -184,10 +183,22 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 
 // cap tanh(x / cap) in log2 units, from x2 = 2 log2(e) x / cap: tanh(u) = 1 - 2 / (e^(2u) + 1). Its error is
-// absolute, about 2^-23 of the cap, which is what a softmax needs of its scores. e^(2u) may overflow: the quotient is
-// then 0. NaN stays.
+// absolute, about 2^-23 of the cap, which is what a softmax needs of its scores as long as the cap is not far above
+// them (kCapFar: 2^-14 there). e^(2u) may overflow: the quotient is then 0. NaN stays.
 __device__ __forceinline__ float capped(float x2, float cap_log2) {
   return cap_log2 - __fdividef(2.0f * cap_log2, ex2_approx(x2) + 1.0f);
+}
+// The same for larger caps: u + u^3 q(u^2) where |u| <= 1, whose error is relative to u (q fitted to the least largest error
+// of tanh, 3.2e-7).
+constexpr float kCapFar = 512.f * kLog2e;
+__device__ __forceinline__ float capped_far(float x2, float cap_log2) {
+  const float u = x2 * 0.34657359f, w = u * u;                   // ln 2 / 2
+  const float q = fmaf(fmaf(fmaf(fmaf(-0.00298308f, w, 0.01653281f), w, -0.05142535f), w, 0.13275615f), w, -0.33328670f);
+  return fabsf(u) <= 1.f ? cap_log2 * fmaf(q * w, u, u) : capped(x2, cap_log2);
+}
+// Out of line, and all of a lane's scores at once, for loops that have no registers to spare for it.
+static __device__ __noinline__ float4 capped_far4(float4 x2, float cap_log2) {
+  return make_float4(capped_far(x2.x, cap_log2), capped_far(x2.y, cap_log2), capped_far(x2.z, cap_log2), capped_far(x2.w, cap_log2));
 }
 #endif
 

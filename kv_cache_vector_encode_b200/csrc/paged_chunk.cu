@@ -104,7 +104,7 @@ __device__ __forceinline__ bool find_unit(const PagedAttendParams& p, const Chun
   x.hkv = (c.unit0 + u) - slot * p.Hkv;
   x.b = c.list[1 + slot];
   x.sq = paged_seq(p, x.b);
-  x.first = x.sq.kv - x.sq.qn;
+  x.first = x.sq.first;
   x.prefix = paged_prefix(p, x.sq, x.b);
   paged_range(p, x.sq, x.first, x.first + x.sq.qn - 1, x.prefix, x.lo, x.hi);
   return true;
@@ -587,6 +587,9 @@ __device__ __forceinline__ float shape(const PagedAttendParams& p, float (&s)[N]
       tanh_poly<N, 2>(s, fu);
     } else if (__all_sync(0xffffffffu, most <= 1.f)) {
       tanh_poly<N, 4>(s, fu);
+    } else if (p.cap_log2 > kCapFar) {                           // one row reaches the cap, others may be far below
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = capped_far(s[i] * f * p.cap2x, 1.f);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) s[i] = capped(s[i] * f * p.cap2x, 1.f);

@@ -130,7 +130,7 @@ __device__ __forceinline__ int row_blocks_of(const PagedAttendParams& p, const P
   const int rows = s.qn * p.g, row0 = rb * p.rows_per_item;
   lo = hi = 0;
   if (row0 >= rows || rows > p.chunk_rows) return 0;
-  const int64_t first = s.kv - s.qn;
+  const int64_t first = s.first;
   const int j0 = row0 == 0 ? 0 : row0 / p.g, j1 = row0 + p.rows_per_item >= rows ? s.qn - 1 : (row0 + p.rows_per_item - 1) / p.g;
   paged_range(p, s, first + j0, first + j1, prefix, lo, hi);
   if (hi <= lo) return 0;      // before lo moves to the start of its block
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
   int64_t pos = start.pos, base = start.base;
   for (int b = start.b; pos < start.end && b < p.B; ++b) {
     const PagedSeq sq = paged_seq(p, b);
-    const int64_t first = sq.kv - sq.qn;                         // position of query 0
+    const int64_t first = sq.first;
     const int64_t prefix = paged_prefix(p, sq, b);
     const int rows = sq.qn * p.g;
     // items in the order of their numbers, so that (CTA + item) grows with every part
@@ -441,12 +441,25 @@ __global__ void __launch_bounds__(32 * kRowWarps, 2) rows_kernel(const __grid_co
               int sc = (ah[u][2 * k] << 8) + ah[u][2 * k + 1] + al[u][2 * k];
               sc += KB == 4 ? (al[u][2 * k + 1] + qsum[u]) >> 8 : al[u][2 * k + 1] >> 8;
               float v = (float)sc * (nk * fac[u]);
-              if (p.cap_log2 > 0.f) v = capped(v * p.cap2x, p.cap_log2);
-              if (p.slopes) v = fmaf(slope[u], (float)(t + r + 8 * k - qpos[u]), v);
+              if (p.cap_log2 > 0.f) {
+                v *= p.cap2x;
+                if (p.cap_log2 <= kCapFar) v = capped(v, p.cap_log2);
+              }
               x[k][u] = v;
               n[k][u] = nv;
               ga[k][u] = ng;
             }
+          }
+          if (p.cap_log2 > kCapFar) {
+            const float4 y = capped_far4(make_float4(x[0][0], x[0][NB - 1], x[1][0], x[1][NB - 1]), p.cap_log2);
+            x[0][NB - 1] = y.y, x[1][NB - 1] = y.w;
+            if (NB > 1) x[0][0] = y.x, x[1][0] = y.z;
+          }
+          if (p.slopes) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int u = 0; u < NB; ++u) x[k][u] = fmaf(slope[u], (float)(t + r + 8 * k - qpos[u]), x[k][u]);
           }
           if (absent != 0 || !((t >= open_lo && t + 16 <= open_hi) || t + 16 <= open_pre)) {
             const bool gone = (absent >> s) & 1;

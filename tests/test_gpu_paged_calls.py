@@ -150,6 +150,21 @@ def test_arguments_past_32_bits_are_refused(dev):
     tq.tq_sync_check()
 
 
+# ---- large caps ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("softcap", [300.0, 1e3, 1e4, 1e6, 1e12, 1e30])
+@pytest.mark.parametrize("q_lens", [[1, 1], [150, 3]])
+def test_attend_large_caps(dev, q_lens, softcap):
+    """A cap far above the scores changes nothing, and takes no precision from them."""
+    Hq, Hkv, d = 8, 2, 128
+    pool = Paged(dev, [400, 90], Hkv, d, 3, 3, 2, 16, seed=17)
+    q = queries(np.random.default_rng(17), sum(q_lens), Hq, d, dev)
+    for scale in (None, 1.0):
+        out = pool.call(q, q_lens, softcap=softcap, scale=scale)
+        tq.tq_sync_check()
+        check(pool, out, q, q_lens, softcap=softcap, scale=scale)
+
+
 # ---- signs next to zero --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("log2_length", [0, 12])

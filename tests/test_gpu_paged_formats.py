@@ -84,3 +84,37 @@ def test_attend_long_context(dev):
         out = pool.call(q, q_lens)
         tq.tq_sync_check()
         check(pool, out, q, q_lens)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,batch,q_len", [
+    (128, 1, 128, 1, 1), (128, 1, 64, 40, 1), (256, 2, 128, 3, 2), (9, 3, 64, 2, 5), (10, 2, 128, 5, 60), (12, 1, 128, 2, 40),
+])
+def test_attend_head_groups(dev, Hq, Hkv, d, batch, q_len):
+    """Up to 128 query heads per KV head (a single token then has as many rows as a chunk), and numbers that divide no
+    block of rows."""
+    rng = np.random.default_rng(Hq + batch)
+    lens = [int(n) for n in rng.integers(q_len, 180, batch)]
+    q_lens = [q_len] * batch
+    pool = Paged(dev, lens, Hkv, d, 3, 3, 2, 32, seed=Hq)
+    q = queries(rng, sum(q_lens) + 2, Hq, d, dev)
+    out = pool.call(q, q_lens, pad=2, window=90)
+    tq.tq_sync_check()
+    check(pool, out, q, q_lens, window=90)
+
+
+@pytest.mark.parametrize("most", [1, 3, 17])
+def test_attend_many_sequences(dev, most):
+    """More sequences than a block has threads, empty ones among them: single tokens, several, and chunks (more than 52
+    query rows per KV head) beside them."""
+    B, Hq, Hkv, d = 700, 8, 2, 64
+    rng = np.random.default_rng(most)
+    lens = rng.integers(0, 90, B)
+    lens[rng.choice(B, 4, replace=False)] = 400, 333, 0, 1
+    q_lens = np.minimum(lens, rng.integers(0, most + 1, B))
+    lens, q_lens = [int(n) for n in lens], [int(n) for n in q_lens]
+    pool = Paged(dev, lens, Hkv, d, 2, 3, 1, 16, seed=most)
+    q = queries(rng, sum(q_lens) + 2, Hq, d, dev)
+    for opt in ({}, dict(window=25)):
+        out = pool.call(q, q_lens, pad=2, **opt)
+        tq.tq_sync_check()
+        check(pool, out, q, q_lens, **opt)
