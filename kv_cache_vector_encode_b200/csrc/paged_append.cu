@@ -629,7 +629,7 @@ extern "C" TQ_API tq_status tq_paged_append(const tq_paged_kv* kv, int64_t token
   if (x_dtype != TQ_F32 && x_dtype != TQ_BF16) return fail(TQ_ERR_UNSUPPORTED, f + ": x_dtype must be TQ_F32 or TQ_BF16");
   if (rot_dim < 0 || rot_dim > kv->d || rot_dim % 2) return fail(TQ_ERR_UNSUPPORTED, f + ": rot_dim must be even, 0..d");
   if (layout != TQ_ROPE_HALF && layout != TQ_ROPE_PAIRS) return fail(TQ_ERR_INVALID_ARG, f + ": unknown layout");
-  if (tokens > 0 && (!k_new || !v_new || !slots || !rot || (rot_dim && (!positions || !table))))
+  if (tokens > 0 && (!k_new || !v_new || !slots || !rot || (rot_dim && (!positions || (!table && n_pos > 0)))))
     return fail(TQ_ERR_INVALID_ARG, f + ": NULL pointer");
   const int64_t row = (int64_t)kv->Hkv * kv->d, unit = x_dtype == TQ_F32 ? 4 : 8;
   if (k_token_stride < row || v_token_stride < row) return fail(TQ_ERR_INVALID_ARG, f + ": token stride < Hkv d");

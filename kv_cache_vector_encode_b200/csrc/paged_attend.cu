@@ -355,7 +355,7 @@ extern "C" TQ_API tq_status tq_paged_attend(const tq_paged_kv* kv, int32_t B, in
   tq_status s = check_sizes(f, kv, B, Hq, total_q, max_q_len, max_kv_len);
   if (s != TQ_OK) return s;
   const bool work = B > 0 && total_q > 0 && max_q_len > 0;
-  if (work && (!q || !q_start || !kv_len || !page_table || !rot || !out)) return fail(TQ_ERR_INVALID_ARG, f + ": NULL pointer");
+  if (work && (!q || !q_start || !kv_len || (!page_table && max_pages > 0) || !rot || !out)) return fail(TQ_ERR_INVALID_ARG, f + ": NULL pointer");
   if (q_dtype != TQ_BF16) return fail(TQ_ERR_UNSUPPORTED, f + ": q must be TQ_BF16");
   if (max_pages < 0 || window < 0) return fail(TQ_ERR_INVALID_ARG, f + ": negative max_pages or window");
   if (!(softcap == 0.0f || softcap >= 1e-30f) || std::isinf(softcap))

@@ -217,7 +217,7 @@ extern "C" TQ_API tq_status tq_rope(int64_t tokens, int32_t heads, int32_t d, in
   clear_error();
   const std::string f = "tq_rope";
   if (tokens < 0 || heads < 1 || n_pos < 0) return fail(TQ_ERR_INVALID_ARG, f + ": negative size");
-  if (tokens > 0 && (!x || !out || !positions || !table)) return fail(TQ_ERR_INVALID_ARG, f + ": NULL pointer");
+  if (tokens > 0 && (!x || !out || !positions || (!table && n_pos > 0))) return fail(TQ_ERR_INVALID_ARG, f + ": NULL pointer");
   if (d < 2 || d > 4096) return fail(TQ_ERR_UNSUPPORTED, f + ": d must be in 2..4096");
   if (rot_dim < 2 || rot_dim > 512 || rot_dim > d || rot_dim % 2)
     return fail(TQ_ERR_UNSUPPORTED, f + ": rot_dim must be even, 2..min(d, 512)");

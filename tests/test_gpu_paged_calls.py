@@ -165,6 +165,27 @@ def test_attend_large_caps(dev, q_lens, softcap):
         check(pool, out, q, q_lens, softcap=softcap, scale=scale)
 
 
+# ---- nothing there -------------------------------------------------------------------------------
+
+def test_calls_without_pages_or_table(dev):
+    """Sequences without tokens need no pages, and rows that only pad the batch no table."""
+    kv = tq.empty_paged(2, 2, 16, 64, 3, 3, device=dev)
+    rot = rotation(64, dev)[2]
+    for q_lens in ([1, 2], [200, 0]):
+        q = queries(np.random.default_rng(0), sum(q_lens) + 1, 4, 64, dev)
+        out = torch.full_like(q, 7.0)
+        tq.tq_paged_attend(kv, q, i32(np.concatenate([[0], np.cumsum(q_lens)]), dev), i32([0, 0], dev),
+                           torch.zeros(2, 0, dtype=torch.int32, device=dev), rot, out, max_q_len=max(q_lens), max_kv_len=0)
+        assert torch.all(out[:-1] == 0) and torch.all(out[-1] == 7)
+    x = torch.ones(3, 2, 64, device=dev)
+    pad, none = i32([-1, -5, -1], dev), tq.tq_rope_table(0, 64)
+    assert torch.equal(tq.tq_rope(x.clone(), pad, none), x)
+    before = [t.clone() for t in kv.tensors]
+    tq.tq_paged_append(kv, x, x, torch.full((3,), -1, dtype=torch.int64, device=dev), rot, positions=pad, table=none)
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(before, kv.tensors))
+    tq.tq_sync_check()
+
+
 # ---- signs next to zero --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("log2_length", [0, 12])
