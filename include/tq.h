@@ -424,7 +424,8 @@ TQ_API size_t tq_paged_attend_workspace_bytes(const tq_paged_kv* kv, int32_t B, 
  * Softmax and sums in fp32. A sequence with few query rows per KV head (Qn Hq / Hkv up to 48, up to 256 where B Hkv is small) meets the codes
  * themselves: its queries and the key levels enter the tensor cores as 16-bit integers, value levels and softmax
  * weights as fp16. A longer chunk's visible tokens are decoded once into fp16 tiles in the workspace, by groups of
- * (sequence, KV head) pairs that share 1 GiB of it (one pair at least: 4 d bytes per token).
+ * (sequence, KV head) pairs that share 1 GiB of it (one pair at least: 4 d bytes per token); values whose norm is below
+ * 2^-21 of the largest seen among the 128 tokens of a tile lose precision there.
  * Hq a multiple of Hkv, Hq / Hkv <= 128, B Hkv up to 65535, max_q_len Hq / Hkv up to 2^24 - 256. B and total_q may be
  * 0. ws: caller device workspace of at least tq_paged_attend_workspace_bytes(...) bytes; calls that may overlap on
  * the GPU (two streams, two captured graphs) need one each. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */

@@ -15,6 +15,7 @@
 // the keys' goes into the score factor. The values' exponent e is added to the scores of the softmax
 // numerators, P = 2^(x + e - M) with the running reference M over x + e, and taken out of the denominators
 // (2^-e sum P): no extra work per element, and P is rounded relative to what a row adds up.
+// Norms down to about 2^-21 of a tile's largest keep the full precision of fp16; below, the last bits of values go.
 //
 // A record with a norm or residual norm that is not finite makes the rows that see it NaN; the tile holds zeros in
 // its place, so that no other row meets it.
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
   __syncthreads();
   const int items = c.units * c.tiles;
   int next = items, next_t = 0;                                  // the tile after the one in hand; this thread's token of it
-  bool next_want = false, next_lo = false;                       // the token is in range; it is seen by someone
+  bool next_want = false;                                        // some query may see the token (others have no say in the exponents)
   int next_page = 0, next_hkv = 0;
   auto locate = [&](int item) {                                  // the first tile from `item` on (in steps of the grid)
     next_want = false;
@@ -185,8 +186,7 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
       const OpenUnit x = u < kOpenUnits ? units[u] : open_unit(p, c, u);
       if (k >= x.tiles) continue;
       next_t = x.t0 + k * kTile + tok;
-      next_want = unpacker && next_t < x.hi;
-      next_lo = next_t >= x.lo;
+      next_want = unpacker && next_t >= x.lo && next_t < x.hi;
       next_hkv = x.hkv;
       if (next_want) next_page = p.table[(int64_t)x.b * p.max_pages + (next_t >> p.page_shift)];
       break;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kOpenThreads, 1)
         sw = __ldg(p.v_signs + rec * G + grp);
         vg = __ldg(p.v_gammas + rec);
       }
-    } else if (next_lo) {
+    } else {
       report_bad_input(p.err);
     }
   };

@@ -88,6 +88,29 @@ def test_attend_rows_that_see_nothing(dev, lens, q_lens, softcap):
         check(pool, out, q, q_lens, softcap=softcap)
 
 
+@pytest.mark.parametrize("q_lens", [[1, 2], [150, 130]])
+def test_attend_norms_of_tokens_that_nobody_sees(dev, q_lens):
+    """Before the window of a sequence's first query records may hold anything: they change no bit, though some share a
+    tile of opened tokens with those that are seen."""
+    lens, Hq, Hkv, d, window = [500, 300], 4, 2, 128, 70
+    pool = Paged(dev, lens, Hkv, d, 3, 3, 2, 16, seed=21)
+    for which in (1, 3):                                         # small norms, so that a large one's exponent shows
+        pool.host[which] = (pool.host[which].astype(np.float32) * 2.0**-14).astype(np.float16)
+    pool.upload()
+    q = queries(np.random.default_rng(21), sum(q_lens), Hq, d, dev)
+    want = pool.call(q, q_lens, window=window)
+    tq.tq_sync_check()
+    check(pool, want, q, q_lens, window=window)
+    for what in (60000.0, np.inf, np.nan):
+        for b, (n, m) in enumerate(zip(lens, q_lens)):
+            t = np.arange(n - m + 1 - window)                    # before the first query's window
+            for which in (1, 3):
+                pool.host[which][pool.table[b, t // 16], :, t % 16] = what
+        pool.upload()
+        assert torch.equal(pool.call(q, q_lens, window=window), want)
+    tq.tq_sync_check()
+
+
 # ---- prefixes out of range -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("window", [0, 31])
