@@ -8,7 +8,8 @@ import numpy as np
 import pytest
 
 import paged_bound as PB
-from test_gpu_paged import CASES, Paged, i32, queries, rotation
+from oracle import paged as OP
+from test_gpu_paged import CASES, DTYPES, Paged, check_append, filled, heads_data, i32, queries, records, rotation
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +119,26 @@ def test_attend_many_sequences(dev, most):
         out = pool.call(q, q_lens, pad=2, **opt)
         tq.tq_sync_check()
         check(pool, out, q, q_lens, **opt)
+
+
+@pytest.mark.parametrize("rot,pairs", [(0, False), (64, False), (64, True), (22, False), (50, True)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bits", [1, 2, 3, 4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_formats(dev, d, bits, dtype, rot, pairs):
+    """Every width of both codebooks, head size and type, with the ways a key is turned."""
+    rng = np.random.default_rng(10 * bits + d + rot)
+    tokens, Hkv, ps, alg = 45, 3, 32, 1 if bits == 4 or pairs else 2
+    kv = filled(dev, 4, Hkv, ps, d, 5 - bits, bits + (alg == 2), alg)
+    before = records(kv)
+    x = torch.from_numpy(np.stack([heads_data(rng, tokens, Hkv, d), heads_data(rng, tokens, Hkv, d)])).to(dev).to(DTYPES[dtype])
+    slots, pos = rng.permutation(4 * ps)[:tokens], rng.integers(0, 900, tokens)
+    slots[7] = -1
+    table = tq.tq_rope_table(900, rot) if rot else None
+    tq.tq_paged_append(kv, x[0], x[1], torch.from_numpy(slots).to(dev), rotation(d, dev)[2],
+                       positions=i32(pos, dev) if rot else None, table=table, layout=int(pairs))
+    tq.tq_sync_check()
+    k = x[0].double().cpu().numpy()
+    if rot:
+        k = OP.rope(k, pos, table.cpu().numpy(), pairs)
+    check_append(kv, before, k, x[1].double().cpu().numpy(), slots, dev, alg)
