@@ -12,7 +12,7 @@
 // than the error, and are decided again by the whole warp with fp64 sums: about one in 10^4.
 //
 // Measured: 8192 tokens of 8 heads of 128 (K 3 bits, V 3 bits by Algorithm 2) 111 us, where all in fp64 on the SIMT cores
-// took 1279; 64 tokens 16.4 us. A tile of values takes 24 thousand cycles, of keys 12 thousand: phases that wait for
+// took 1279; 64 tokens 16.1 us (the kernel alone). A tile of values takes 24 thousand cycles, of keys 12 thousand: phases that wait for
 // one another (2000 to 3000 each for the three products, 5000 for the indices), tensor pipe 12 %, issue 32 %.
 //
 // Layout: a CTA takes tiles of 128 vectors (keys or values of consecutive heads and tokens), thread = (vector, group of

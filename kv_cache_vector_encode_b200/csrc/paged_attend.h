@@ -59,9 +59,11 @@ struct PagedSeq {
 // The chunk kernels (paged_chunk.cu): their share of the workspace, and the launch.
 // Query rows per KV head up to which a sequence is a decode step. Eight rows of a step cost 8.4 ns per 128 tokens of a
 // KV head, whatever the batch. A chunk costs 34 ns for opening as many tokens and the time of their scores: 1.9 us,
-// on as many SMs as there are (sequence, KV head) units, at least 13 ns. Measured (step against chunk, us): 16 sequences of
-// 4096 tokens, 8 KV heads: 174 / 249 at 32 rows, 248 / 249 at 48, 464 / 250 at 96; 4 of 16384: 262 / 387 at 64,
-// 381 / 390 at 96; one of 8192: 107 / 148 at 128 rows, 182 / 187 at 256.
+// on as many SMs as there are (sequence, KV head) units, at least 13 ns. Measured (step against chunk, us; d = 128, K 3 bits,
+// V 2 by Algorithm 2, 32 heads over 8): 16 sequences of 4096 tokens 173 / 226 at 32 rows, 245 / 226 at 48, 454 / 227 at
+// 96; 4 of 16384: 255 / 364 at 64, 371 / 366 at 96; one of 8192: 107 / 150 at 128 rows, 182 / 179 at 256. The costs are
+// those of this format. Others meet nearer or further: at 48 rows of 16 sequences 203 / 166 (d = 64, K 4, V 4),
+// 228 / 208 (K 2, V 2), 336 / 235 (K 4, V 4 by Algorithm 2, the largest loss measured).
 inline int paged_chunk_rows(int units) {
   const int rows = 8 * (int)((34.0f + 1900.0f / (float)units) / 8.4f);
   return rows < 48 ? 48 : rows > 256 ? 256 : rows;

@@ -20,8 +20,8 @@
 // A record with a norm or residual norm that is not finite makes the rows that see it NaN; the tile holds zeros in
 // its place, so that no other row meets it.
 //
-// Measured: a chunk of 2048 queries over 8192 tokens (32 heads over 8, V by Algorithm 2) 305 us, 778 TFLOP/s, of which
-// opening takes 25 (512 tiles); twice 2048 over 16384 tokens with a cap 1590 us, 650 TFLOP/s. A step of 256 rows x 128
+// Measured: a chunk of 2048 queries over 8192 tokens (32 heads over 8, V by Algorithm 2) 306 us, 774 TFLOP/s, of which
+// opening takes 25 (512 tiles); twice 2048 over 16384 tokens with a cap 1615 us, 640 TFLOP/s. A step of 256 rows x 128
 // tokens takes about 3700 cycles, five sixths of which the tensor cores' operand traffic needs, at 1.4 GHz under load.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -33,8 +33,8 @@
 // accumulators are rarely rescaled; weights stay below 2^8. The value norms enter the weights, relative to the
 // largest norm seen so far (a power of two, kept with the reference), so that fp16 holds them.
 //
-// Measured: one step of 16 sequences of up to 32768 tokens (32 query heads over 8, K 3 bits, V 2) 158 us with prep and
-// combine, 1.8 TB/s of packed records; 450 warp instructions per 16 tokens, integer pipe 59 %, tensor pipe 24 %. Two
+// Measured: one step of 16 sequences of up to 32768 tokens (32 query heads over 8, K 3 bits, V 2) 154 us with prep and
+// combine, 1.8 TB/s of packed records; 420 warp instructions per 16 tokens, integer pipe 57 %, tensor pipe 25 %. Two
 // CTAs of eight warps per SM: three at 80 registers gain nothing (177 against 172 us).
 #pragma once
 #include <cuda_fp16.h>

@@ -9,8 +9,9 @@
 // heads are spread over more units (down to one head each), so that the loads of a decode step are
 // all in flight at once.
 //
-// Measured: 8192 tokens x 40 heads x 128 in bf16 31.5 us (5.3 TB/s, 0.81 of the copy rate), 4099 x 32 x 64 in fp32 with 48
-// coordinates turned in pairs 18.0 us (3.7 TB/s), 64 tokens x 40 heads 2.5 us.
+// Measured, the kernel alone (40 calls in a captured graph): 8192 tokens x 40 heads x 128 in bf16 31.8 us (5.4 TB/s, 0.82 of
+// the copy rate), 4099 x 32 x 64 in fp32 with 48 coordinates turned in pairs 17.4 us (3.9 TB/s), 64 tokens x 40 heads
+// 2.4 us. A call among others, the host's time included, takes 34.4, 19.9 and 7.8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -156,8 +157,9 @@ tq_status launch_rope(RopeParams& p, int d, bool half_layout, bool in_place, cud
   p.turn_runs = p.half / np;
   p.rest0 = rot;
   p.runs = p.turn_runs + (in_place ? 0 : (d - rot) / nv);
-  // as many units as run at a time (eight blocks of 256 per SM), not more: each reads its part of the table once, and
-  // a second wave of a few blocks costs as much as the first
+  // as many units as eight blocks of 256 per SM hold, not more: each reads its part of the table once. The fp32 pair
+  // kernel (32 registers) runs so many at a time; the others run five (16-bit half layout, 48 registers) or six (40), so
+  // that there a prompt's blocks take a second, shorter wave (8192 tokens x 40 heads in bf16: 1024 blocks in 740 places)
   const int64_t want = (int64_t)sm_count() * 8 * 256, fit = want / (p.tokens * p.runs);
   const int splits = (int)(fit < 1 ? 1 : fit < p.heads ? fit : p.heads);
   const int each = (p.heads + splits - 1) / splits;              // heads of a unit

@@ -90,7 +90,7 @@ def test_results_made_on_another_stream(dev):
     for t in late:
         t.fill_(255)
     del late, t
-    table = tq.tq_rope_table(n, rot_dim, stream=side)
+    table = tq.tq_rope_table(n, rot_dim, stream=side.cuda_stream)
     rot = tq.tq_rotation_prepare(Pi, S, stream=side)
     torch.cuda.synchronize()
     exact = OP.rope_table(n, OP.rope_freqs(rot_dim))
