@@ -142,3 +142,16 @@ def test_append_formats(dev, d, bits, dtype, rot, pairs):
     if rot:
         k = OP.rope(k, pos, table.cpu().numpy(), pairs)
     check_append(kv, before, k, x[1].double().cpu().numpy(), slots, dev, alg)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [100, 1, 90]])
+def test_attend_shared_pages(dev, q_lens):
+    """Sequences that begin with the same pages, and one that names a page twice."""
+    Hq, Hkv, d, ps = 8, 2, 128, 32
+    pool = Paged(dev, [300, 280, 260], Hkv, d, 3, 3, 2, ps, seed=30)
+    pool.table[1, :5] = pool.table[0, :5]
+    pool.table[2, 3:7] = pool.table[0, [0, 0, 8, 2]]
+    q = queries(np.random.default_rng(30), sum(q_lens) + 2, Hq, d, dev)
+    out = pool.call(q, q_lens, pad=2)
+    tq.tq_sync_check()
+    check(pool, out, q, q_lens)

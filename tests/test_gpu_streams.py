@@ -97,3 +97,92 @@ def test_results_made_on_another_stream(dev):
     assert np.max(np.abs(table.cpu().numpy() - exact)) <= 2.0**-24 + 1e-10
     used = slice(0, 8)                                           # header; then the fp32 matrices, 256 bytes in
     assert torch.equal(rot[used], want[used]) and torch.equal(rot[256:256 + 3 * d * d * 4], want[256:256 + 3 * d * d * 4])
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [180, 2]])
+def test_a_captured_step_follows_its_inputs(dev, q_lens):
+    """Turn, append and attend captured together on a stream of their own and replayed with other inputs, positions, slots
+    and lengths in place; twice over, with a replay of each graph in turn."""
+    Hq, Hkv, d, ps, pages = 8, 2, 128, 16, 30
+    rng = np.random.default_rng(6)
+    rot = rotation(d, dev)[2]
+    table = tq.tq_rope_table(600, d)
+    rows = sum(q_lens)
+    order = rng.permutation(2 * pages).reshape(2, pages)
+    start, page_table = i32(np.concatenate([[0], np.cumsum(q_lens)]), dev), i32(order, dev)
+    caches = [tq.empty_paged(2 * pages, Hkv, ps, d, 3, 3, 2, device=dev) for _ in range(3)]
+    for kv in caches:
+        for t in kv.tensors:
+            t.zero_()
+
+    class Inputs:
+        def __init__(self):
+            self.qkv = torch.zeros(rows, Hq + 2 * Hkv, d, dtype=torch.bfloat16, device=dev)
+            self.pos, self.lens = torch.zeros(rows, dtype=torch.int32, device=dev), torch.zeros(2, dtype=torch.int32, device=dev)
+            self.slots = torch.zeros(rows, dtype=torch.int64, device=dev)
+            self.out = torch.zeros(rows, Hq, d, dtype=torch.bfloat16, device=dev)
+
+        def fill(self, data, lens):
+            pos = np.concatenate([n - m + np.arange(m) for n, m in zip(lens, q_lens)])
+            seq = np.repeat(np.arange(2), q_lens)
+            self.qkv.copy_(data)
+            self.pos.copy_(i32(pos, dev))
+            self.lens.copy_(i32(lens, dev))
+            self.slots.copy_(torch.from_numpy(order[seq, pos // ps] * ps + pos % ps))
+
+        def step(self, kv):
+            q, k, v = self.qkv[:, :Hq], self.qkv[:, Hq:Hq + Hkv], self.qkv[:, Hq + Hkv:]
+            tq.tq_rope(q, self.pos, table)
+            tq.tq_paged_append(kv, k, v, self.slots, rot, positions=self.pos, table=table)
+            tq.tq_paged_attend(kv, q, start, self.lens, page_table, rot, self.out, max_q_len=max(q_lens), max_kv_len=400)
+
+    plain, held = Inputs(), [Inputs(), Inputs()]
+    plain.step(caches[0])                                        # warm-up: nothing is loaded during the capture
+    graphs = []
+    for x, kv in zip(held, caches[1:]):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            x.step(kv)
+        graphs.append(g)
+    for kv in caches:
+        for t in kv.tensors:
+            t.zero_()
+    for n in range(3):
+        data, lens = queries(rng, rows, Hq + 2 * Hkv, d, dev), [200 + 31 * n, 190 + n]
+        for x in (plain, *held):
+            x.fill(data, lens)
+        plain.step(caches[0])
+        for g in graphs:
+            g.replay()
+        for x, kv in zip(held, caches[1:]):
+            assert torch.equal(x.out, plain.out) and torch.equal(x.qkv, plain.qkv)
+            assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(kv.tensors, caches[0].tensors))
+    tq.tq_sync_check()
+
+
+def test_calls_from_two_threads(dev):
+    """Host threads with streams of their own, and each the message of its own failure."""
+    import threading
+    Hq, Hkv, d = 8, 2, 128
+    pool = Paged(dev, [900, 333], Hkv, d, 3, 3, 2, 32, seed=8)
+    jobs = [(queries(np.random.default_rng(8), sum(m), Hq, d, dev), m) for m in ([1, 1], [150, 7])]
+    wants = [pool.call(q, m) for q, m in jobs]
+    torch.cuda.synchronize()
+    results, table = [[], []], tq.tq_rope_table(9, d)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                results[i].append(torch.equal(pool.call(*jobs[i]), wants[i]))
+                try:
+                    tq.tq_rope(jobs[i][0], i32(np.zeros(len(jobs[i][0])), dev), table, layout=5) if i else pool.call(*jobs[i], window=-1)
+                except tq.TQError as e:
+                    results[i].append(("layout" if i else "window") in str(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert [len(r) for r in results] == [40, 40] and all(map(all, results))
+    tq.tq_sync_check()
