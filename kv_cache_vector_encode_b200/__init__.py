@@ -19,6 +19,7 @@ Names follow the C ABI. Tensors:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -204,6 +205,7 @@ def tq_codebook_init(d: int, bits: int) -> Codebook:
     return cb
 
 
+@functools.lru_cache(maxsize=None)           # every call that takes a rotation asks for it
 def tq_rotation_bytes(d: int) -> int:
     return int(lib().tq_rotation_bytes(d))
 
